@@ -28,8 +28,15 @@ EXPORTED = [
     "uw_encode", "uw_decode", "uw_matmul", "uw_preprocess", "uw_set_streams", "uw_set_scratch", "uw_set_plan",
     "uw_set_variant", "uw_variant_name", "uw_variant_in_use", "uw_query", "uw_export", "uw_clone", "uw_save", "uw_load", "uw_upload", "uw_evict", "uw_grouped_matmul", "uw_free", "uw_last_error", "uw_silu_mul",
     "uw_mlp_forward", "uw_mlp_workspace_bytes", "uw_mlp_forward_noalloc", "uw_stack_forward", "uw_stack_workspace_bytes",
-    "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
+    "uw_route", "uw_group_rows_workspace_bytes", "uw_group_rows", "uw_dispatch_rows", "uw_combine_rows",
+    "uw_moe_workspace_bytes", "uw_moe_forward", "uw_lora_create", "uw_lora_load", "uw_lora_free", "uw_lora_plan_bytes",
+    "uw_lora_plan", "uw_lora_workspace_bytes", "uw_lora_apply", "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
 ]
+
+F32, BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+LORA_MAX_RANK = 256  # UW_LORA_MAX_RANK
 
 
 class UwError(RuntimeError):
@@ -46,6 +53,13 @@ class Info(C.Structure):
         ("stream_bits", C.c_uint64), ("stream_words", C.c_uint64), ("bpw_palette", C.c_double),
         ("bpw_huffman", C.c_double), ("bpw_resident", C.c_double), ("resident_bytes", C.c_uint64),
         ("scratch_bytes", C.c_uint64 * 6), ("max_row_raw", C.c_uint32),
+    ]
+
+
+class RouteConfig(C.Structure):
+    _fields_ = [
+        ("experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("groups", C.c_int32),
+        ("top_groups", C.c_int32), ("group_score", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float),
     ]
 
 
@@ -97,6 +111,22 @@ def _load() -> C.CDLL:
         "uw_mlp_forward_noalloc": ([vp, vp, vp, C.POINTER(i32), vp, vp, i64], st),
         "uw_stack_forward": ([C.POINTER(vp), C.POINTER(i32), i32, vp, vp, i64, i32, vp, C.c_size_t], st),
         "uw_stack_workspace_bytes": ([i64, i64, i64], C.c_size_t),
+        "uw_route": ([vp, i32, i64, i64, vp, C.POINTER(RouteConfig), vp, vp, vp], st),
+        "uw_group_rows_workspace_bytes": ([i64, i32], C.c_size_t),
+        "uw_group_rows": ([vp, i64, i32, vp, vp, vp, vp, C.c_size_t, vp], st),
+        "uw_dispatch_rows": ([vp, i64, vp, i64, i32, i64, vp, i64, vp], st),
+        "uw_combine_rows": ([vp, i64, vp, vp, i64, i32, i64, vp, vp, i32, vp], st),
+        "uw_moe_workspace_bytes": ([i64, i64, i64, i32, i32], C.c_size_t),
+        "uw_moe_forward": ([C.POINTER(vp), C.POINTER(i32), vp, i32, i64, vp, C.POINTER(RouteConfig), vp, vp, vp, i64,
+                            vp, C.c_size_t], st),
+        "uw_lora_create": ([i64, i64, i32, i32, C.POINTER(vp)], st),
+        "uw_lora_load": ([vp, i32, vp, vp, i32, C.c_float, vp], st),
+        "uw_lora_free": ([vp], None),
+        "uw_lora_plan_bytes": ([i64, i32], C.c_size_t),
+        "uw_lora_plan": ([vp, i64, i32, vp, C.c_size_t, vp], st),
+        "uw_lora_workspace_bytes": ([C.POINTER(vp), i32, i64], C.c_size_t),
+        "uw_lora_apply": ([C.POINTER(vp), i32, vp, C.c_size_t, vp, i64, C.POINTER(vp), C.POINTER(i64), C.POINTER(vp),
+                           C.POINTER(i64), i64, vp, C.c_size_t, vp], st),
         "uw_stream_create": ([i32, i32, C.POINTER(vp)], st),
         "uw_stream_destroy": ([vp], st),
         "uw_device_cu_count": ([], i32),
@@ -353,3 +383,194 @@ def grouped_matmul(experts, x, y, row_offsets, pipeline: int = P_AUTO) -> None:
     hs = (C.c_void_p * n)(*[m.handle for m in experts])
     offs = (C.c_int64 * (n + 1))(*[int(v) for v in row_offsets])
     _check(_lib.uw_grouped_matmul(hs, n, _ptr(x), offs, _ptr(y), pipeline))
+
+
+# ---- routing of tokens to experts and back, low-rank adapters ----
+#
+# These calls check what the C side cannot see of a tensor: its type, shape,
+# strides and device.
+
+
+def _tensor(t, name: str, dtypes: str, *shape, rows_strided: bool = False):
+    """``t`` as a tensor of one of the types named, on the current device, of this
+    shape (None: any size) and contiguous (or, rows_strided, with contiguous rows)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if str(t.dtype)[6:] not in dtypes.split("|"):
+        raise TypeError(f"{name} must be {dtypes}, not {t.dtype}")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not (t.is_contiguous() or (rows_strided and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1])):
+        raise ValueError(f"{name} must be contiguous" + (" along its rows" if rows_strided else ""))
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU, not {t.device}")
+    return t.data_ptr()
+
+
+def _stride(t) -> int:
+    """Row stride in elements (a single row's stride does not matter)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _bytes(t, name: str) -> tuple[int, int]:
+    """Address and size of a workspace tensor of any type and shape (None: 0, 0)."""
+    if t is None:
+        return 0, 0
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device() or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on the current GPU")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _route_config(experts, top_k, score, groups, top_groups, group_score, renormalise, scale) -> RouteConfig:
+    return RouteConfig(experts, top_k, score, groups, top_groups, group_score, int(bool(renormalise)), scale)
+
+
+def route(logits, experts, weights, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
+          group_score: int = GROUP_MAX, renormalise: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Choose each token's experts (``uw_route``): logits [tokens, E] float32 or
+    bfloat16 -> experts [tokens, top_k] int32 and weights [tokens, top_k] float32."""
+    lp = _tensor(logits, "logits", "float32|bfloat16", None, None, rows_strided=True)
+    t, e = logits.shape
+    ep = _tensor(experts, "experts", "int32", t, None)
+    k = experts.shape[1]
+    cfg = _route_config(e, k, score, groups, top_groups, group_score, renormalise, scale)
+    _check(_lib.uw_route(lp, F32 if logits.element_size() == 4 else BF16, _stride(logits), t,
+                         0 if bias is None else _tensor(bias, "bias", "float32", e), C.byref(cfg), ep,
+                         _tensor(weights, "weights", "float32", t, k), _stream_ptr(stream)))
+
+
+def group_rows_workspace_bytes(n: int, groups: int) -> int:
+    return _lib.uw_group_rows_workspace_bytes(n, groups)
+
+
+def group_rows(index, groups: int, offsets, order, slot, work=None, stream=None) -> None:
+    """Stable counting sort of index (int32, any shape, n entries) into groups
+    (``uw_group_rows``): offsets [groups + 1], order [n] and slot (index's shape), int32."""
+    ip = _tensor(index, "index", "int32", *index.shape)
+    n = index.numel()
+    wp, wb = _bytes(work, "work")
+    _check(_lib.uw_group_rows(ip, n, groups, _tensor(offsets, "offsets", "int32", groups + 1),
+                              _tensor(order, "order", "int32", n), _tensor(slot, "slot", "int32", *index.shape), wp, wb,
+                              _stream_ptr(stream)))
+
+
+def dispatch_rows(x, slot, xs, stream=None) -> None:
+    """xs[slot[t, j]] = x[t] (``uw_dispatch_rows``): x [tokens, cols] bfloat16, slot
+    [tokens, top_k] int32, xs [rows, cols] bfloat16."""
+    xp = _tensor(x, "x", "bfloat16", None, None, rows_strided=True)
+    t, c = x.shape
+    sp = _tensor(slot, "slot", "int32", t, None)
+    op = _tensor(xs, "xs", "bfloat16", None, c)
+    _check(_lib.uw_dispatch_rows(xp, _stride(x), sp, t, slot.shape[1], c, op, xs.shape[0], _stream_ptr(stream)))
+
+
+def combine_rows(ys, slot, weights, y, base=None, stream=None) -> None:
+    """y[t] = base[t] + sum_j weights[t, j] * ys[slot[t, j]] (``uw_combine_rows``): ys
+    [rows, cols] float32, y [tokens, cols] float32 or bfloat16, base float32 or None."""
+    yp = _tensor(ys, "ys", "float32", None, None)
+    rows, c = ys.shape
+    sp = _tensor(slot, "slot", "int32", None, None)
+    t, k = slot.shape
+    op = _tensor(y, "y", "float32|bfloat16", t, c)
+    _check(_lib.uw_combine_rows(yp, rows, sp, _tensor(weights, "weights", "float32", t, k), t, k, c,
+                                0 if base is None else _tensor(base, "base", "float32", t, c), op,
+                                F32 if y.element_size() == 4 else BF16, _stream_ptr(stream)))
+
+
+def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    return _lib.uw_moe_workspace_bytes(tokens, hidden, inter, experts, top_k)
+
+
+def moe_forward(mats, pipelines, logits, x, y, work, top_k: int, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1,
+                top_groups: int = 1, group_score: int = GROUP_MAX, renormalise: bool = True, scale: float = 1.0,
+                base=None) -> None:
+    """A layer of SwiGLU experts (``uw_moe_forward``) on the experts' main stream.
+    mats: flat list [gate0, up0, down0, gate1, ...]; logits [tokens, E]."""
+    n = len(mats)
+    if n == 0 or n % 3:
+        raise ValueError("mats must hold gate, up and down of each expert")
+    lp = _tensor(logits, "logits", "float32|bfloat16", None, n // 3, rows_strided=True)
+    t, hidden = logits.shape[0], mats[0].cols
+    cfg = _route_config(n // 3, top_k, score, groups, top_groups, group_score, renormalise, scale)
+    wp, wb = _bytes(work, "work")
+    _check(_lib.uw_moe_forward((C.c_void_p * n)(*[m.handle for m in mats]), (C.c_int32 * 3)(*pipelines), lp,
+                               F32 if logits.element_size() == 4 else BF16, _stride(logits),
+                               0 if bias is None else _tensor(bias, "bias", "float32", n // 3), C.byref(cfg),
+                               _tensor(x, "x", "bfloat16", t, hidden),
+                               0 if base is None else _tensor(base, "base", "float32", t, hidden),
+                               _tensor(y, "y", "float32", t, hidden), t, wp, wb))
+
+
+class Adapters:
+    """Low-rank adapters of one projection in numbered slots (a ``uw_lora``)."""
+
+    def __init__(self, slots: int, rows: int, cols: int, max_rank: int):
+        h = C.c_void_p()
+        self._h = h
+        _check(_lib.uw_lora_create(rows, cols, slots, max_rank, C.byref(h)))
+        self.slots, self.rows, self.cols, self.max_rank = slots, rows, cols, max_rank
+
+    @property
+    def handle(self) -> int:
+        return self._h.value
+
+    def load(self, slot: int, a, b, scale: float = 1.0, stream=None) -> None:
+        """Copy A [rank, cols] and B [rows, rank] (bfloat16, on the GPU) into a slot (``uw_lora_load``)."""
+        ap = _tensor(a, "a", "bfloat16", None, self.cols)
+        bp = _tensor(b, "b", "bfloat16", self.rows, a.shape[0])
+        _check(_lib.uw_lora_load(self._h, slot, ap, bp, a.shape[0], scale, _stream_ptr(stream)))
+
+    def clear(self, slot: int, stream=None) -> None:
+        """Empty a slot: its tokens have no adapter."""
+        _check(_lib.uw_lora_load(self._h, slot, None, None, 0, 0.0, _stream_ptr(stream)))
+
+    def free(self) -> None:
+        if self._h:
+            _lib.uw_lora_free(self._h)
+            self._h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def lora_plan_bytes(tokens: int, slots: int) -> int:
+    return _lib.uw_lora_plan_bytes(tokens, slots)
+
+
+def lora_plan(index, slots: int, plan, stream=None) -> None:
+    """Sort a batch's tokens by adapter slot (``uw_lora_plan``): index [tokens] int32."""
+    ip = _tensor(index, "index", "int32", None)
+    pp, pb = _bytes(plan, "plan")
+    _check(_lib.uw_lora_plan(ip, index.shape[0], slots, pp, pb, _stream_ptr(stream)))
+
+
+def lora_workspace_bytes(adapters, tokens: int) -> int:
+    n = len(adapters)
+    return _lib.uw_lora_workspace_bytes((C.c_void_p * n)(*[a.handle for a in adapters]), n, tokens)
+
+
+def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
+    """ys[i] = bases[i] + scale * B (A x) per token for each projection's ``Adapters``
+    (``uw_lora_apply``); bases None: in place, on top of what ys hold.  A base
+    may be None by itself (zeros)."""
+    n = len(adapters)
+    if bases is None:
+        bases = ys
+    if len(ys) != n or len(bases) != n:
+        raise ValueError("adapters, ys and bases must have one length")
+    xp = _tensor(x, "x", "bfloat16", None, adapters[0].cols if n else None, rows_strided=True)
+    t = x.shape[0]
+    yp = [_tensor(y, "ys", "float32", t, a.rows, rows_strided=True) for a, y in zip(adapters, ys)]
+    bp = [None if b is None else _tensor(b, "bases", "float32", t, a.rows, rows_strided=True)
+          for a, b in zip(adapters, bases)]
+    pp, pb = _bytes(plan, "plan")
+    wp, wb = _bytes(work, "work")
+    _check(_lib.uw_lora_apply((C.c_void_p * n)(*[a.handle for a in adapters]), n, pp, pb, xp, _stride(x),
+                              (C.c_void_p * n)(*bp), (C.c_int64 * n)(*[0 if b is None else _stride(b) for b in bases]),
+                              (C.c_void_p * n)(*yp), (C.c_int64 * n)(*[_stride(y) for y in ys]), t, wp, wb,
+                              _stream_ptr(stream)))

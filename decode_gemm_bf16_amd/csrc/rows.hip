@@ -1,0 +1,245 @@
+// Rows grouped by an index (a token's experts, a request's adapter), copied to
+// their groups and combined on the way back.
+#include "recon.h"
+#include "routing.h"
+
+namespace uw {
+namespace {
+
+__device__ __forceinline__ uint16_t to_bf16(float f) {  // round to nearest even, NaN stays NaN
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+  return (uint16_t)((u + (((u >> 16) & 1u) + 0x7FFFu)) >> 16);
+}
+
+// ---- grouping: a stable counting sort ----
+//
+// The entries are cut into one section per wave, in order.  Each wave counts
+// its section's labels (label = group, or `groups` for ungrouped entries) into
+// its own row of LDS counters; a prefix sum over the waves and then over the
+// labels turns the counters into each (wave, label)'s first position; each
+// wave then walks its section again, 64 entries at a time, and an entry's
+// position is its counter plus its rank among the equal labels of the 64.  No
+// position depends on the order in which atomics are served.
+//
+// Up to kOneBlock entries one workgroup does all of it.  Beyond, a first
+// kernel writes each workgroup's counts and in the second each workgroup sums
+// the counts of those before it by itself.
+
+constexpr int64_t kOneBlock = 8192;
+constexpr int kMaxBlocks = 256;
+
+int waves_of(int32_t groups) { return groups < 1000 ? 16 : groups < 2000 ? 8 : 4; }  // counters within 64 KB
+
+// Entries per workgroup: a multiple of 64 per wave, at most kMaxBlocks of them.
+int64_t chunk_of(int64_t n, int waves) {
+  const int64_t step = 64 * waves;
+  if (n <= kOneBlock) return (n + step - 1) / step * step;
+  const int64_t want = (n + kMaxBlocks - 1) / kMaxBlocks, least = 4 * step;
+  const int64_t c = want > least ? want : least;
+  return (c + step - 1) / step * step;
+}
+
+__device__ __forceinline__ int label_of(const GroupArgs& a, int64_t i) {
+  const int32_t v = a.index[i];
+  return (uint32_t)v < (uint32_t)a.groups ? v : a.groups;
+}
+
+__device__ __forceinline__ void count_section(const GroupArgs& a, int* ctr, int64_t lo, int64_t hi, int lane) {
+  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&ctr[label_of(a, i)], 1);
+}
+
+__global__ __launch_bounds__(1024) void group_count_kernel(GroupArgs a, int64_t chunk) {
+  extern __shared__ int ctr[];  // [groups + 1]
+  const int labels = a.groups + 1;
+  for (int g = threadIdx.x; g < labels; g += blockDim.x) ctr[g] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < a.n ? lo + chunk : a.n;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) atomicAdd(&ctr[label_of(a, i)], 1);
+  __syncthreads();
+  for (int g = threadIdx.x; g < labels; g += blockDim.x) a.work[(int64_t)blockIdx.x * labels + g] = ctr[g];
+}
+
+// Exclusive sum of v over the workgroup's threads; wsum: LDS for 16 waves.
+__device__ __forceinline__ int block_scan(int v, int* wsum) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int x = v;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) wsum[w] = x;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < nw; ++i) before += i < w ? wsum[i] : 0;
+  return before + x - v;
+}
+
+template <bool MULTI>
+__global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t chunk) {
+  extern __shared__ int ctr[];  // [waves][groups + 1]
+  __shared__ int wsum[16];
+  const int labels = a.groups + 1, nw = blockDim.x >> 6, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int i = threadIdx.x; i < nw * labels; i += blockDim.x) ctr[i] = 0;
+  __syncthreads();
+  const int64_t sec = chunk / nw;
+  const int64_t lo = blockIdx.x * chunk + w * sec, hi = lo + sec < a.n ? lo + sec : a.n;
+  count_section(a, ctr + w * labels, lo, hi, lane);
+  __syncthreads();
+  // this thread's labels, their counts over all entries and in the workgroups before
+  const int per = (labels + blockDim.x - 1) / blockDim.x;
+  const int g0 = threadIdx.x * per, g1 = g0 + per < labels ? g0 + per : labels;
+  auto all_of = [&](int g) {
+    int c = 0;
+    if (MULTI) {
+      for (int b = 0; b < (int)gridDim.x; ++b) c += a.work[(int64_t)b * labels + g];
+    } else {
+      for (int i = 0; i < nw; ++i) c += ctr[i * labels + g];
+    }
+    return c;
+  };
+  int sum = 0, tiles = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int c = all_of(g);
+    sum += c;
+    tiles += (c + kPlanTile - 1) / kPlanTile;
+  }
+  int base = block_scan(sum, wsum);
+  const bool plan = a.header && blockIdx.x == 0;
+  int tile = plan ? block_scan(tiles, wsum) : 0;
+  for (int g = g0; g < g1; ++g) {
+    const int c = all_of(g);
+    if (blockIdx.x == 0 && a.offsets) a.offsets[g] = base;
+    if (plan)
+      for (int r = 0; r < c; r += kPlanTile)
+        a.tiles[tile++] = PlanTile{base + r, c - r < kPlanTile ? c - r : kPlanTile, g < a.groups ? g : -1, 0};
+    int run = base;
+    if (MULTI)
+      for (int b = 0; b < (int)blockIdx.x; ++b) run += a.work[(int64_t)b * labels + g];
+    for (int i = 0; i < nw; ++i) {
+      const int v = ctr[i * labels + g];
+      ctr[i * labels + g] = run;
+      run += v;
+    }
+    base += c;
+    if (plan && g == labels - 1) *a.header = PlanHeader{(int32_t)a.n, a.groups, tile, 0};
+  }
+  __syncthreads();
+  int bits = 0;
+  while ((1 << bits) < labels) ++bits;
+  int* mine = ctr + w * labels;
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool there = i < hi;
+    const int g = there ? label_of(a, i) : 0;
+    uint64_t same = __ballot(there);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((g >> b) & 1);
+      same &= (g >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    if (there) {
+      const int at = mine[g] + rank;
+      a.order[at] = (int32_t)i;
+      if (a.slot) a.slot[i] = g < a.groups ? at : -1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (there && rank == 0) mine[g] += __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---- dispatch and combine ----
+
+// One workgroup copies 2048 columns of one token's row to its top_k places:
+// the row is read once, whatever top_k is.
+__global__ __launch_bounds__(256) void dispatch_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                       const int32_t* __restrict__ slot, int64_t tokens, int top_k,
+                                                       int64_t cols, uint16_t* __restrict__ xs, uint32_t rows) {
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= cols) return;
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const u32x4 v = *(const u32x4*)(x + t * ldx + c);
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t at = slot[t * top_k + j];
+      if ((uint32_t)at < rows) *(u32x4*)(xs + at * cols + c) = v;
+    }
+  }
+}
+
+// One workgroup: 1024 columns of one token.  y may be base (each element is
+// read before it is written, by one lane).  Sums in float32, top_k terms in
+// order; entries without a row (slot outside 0..rows-1) add nothing.
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ ys, const int32_t* __restrict__ slot,
+                                                      const float* __restrict__ weight, int64_t tokens, int top_k,
+                                                      int64_t cols, uint32_t rows, const float* base, void* y) {
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= cols) return;
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t at = slot[t * top_k + j];
+      if ((uint32_t)at >= rows) continue;
+      const float w = weight[t * top_k + j];
+      const f32x4 v = *(const f32x4*)(ys + at * cols + c);
+      s += w * v;
+    }
+    if (base) s += *(const f32x4*)(base + t * cols + c);
+    if (BF16)
+      *(u32x2*)((uint16_t*)y + t * cols + c) =
+          u32x2{to_bf16(s.x) | (uint32_t)to_bf16(s.y) << 16, to_bf16(s.z) | (uint32_t)to_bf16(s.w) << 16};
+    else
+      *(f32x4*)((float*)y + t * cols + c) = s;
+  }
+}
+
+// A grid of at most 2^20 workgroups along the tokens (HIP bounds a grid to
+// 2^32 threads); the kernels stride over the rest.
+unsigned token_blocks(int64_t tokens) { return (unsigned)(tokens < (1 << 20) ? tokens : (1 << 20)); }
+
+}  // namespace
+
+size_t group_work_bytes(int64_t n, int32_t groups) {
+  if (n <= kOneBlock) return 0;
+  const int64_t chunk = chunk_of(n, waves_of(groups));
+  return size_t((n + chunk - 1) / chunk) * size_t(groups + 1) * 4;
+}
+
+hipError_t launch_group_rows(const GroupArgs& a, hipStream_t s) {
+  const int waves = waves_of(a.groups), labels = a.groups + 1;
+  const int64_t chunk = chunk_of(a.n, waves);
+  const size_t lds = size_t(waves) * labels * 4;
+  if (a.n <= kOneBlock) {
+    hipLaunchKernelGGL(group_place_kernel<false>, dim3(1), dim3(64 * waves), lds, s, a, chunk);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)((a.n + chunk - 1) / chunk));
+  hipLaunchKernelGGL(group_count_kernel, grid, dim3(64 * waves), size_t(labels) * 4, s, a, chunk);
+  hipLaunchKernelGGL(group_place_kernel<true>, grid, dim3(64 * waves), lds, s, a, chunk);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_rows(const uint16_t* x, int64_t ldx, const int32_t* slot, int64_t tokens, int32_t top_k,
+                                int64_t cols, uint16_t* xs, int64_t rows, hipStream_t s) {
+  const dim3 grid(token_blocks(tokens), (unsigned)((cols + 2047) / 2048));
+  hipLaunchKernelGGL(dispatch_kernel, grid, dim3(256), 0, s, x, ldx, slot, tokens, (int)top_k, cols, xs,
+                     (uint32_t)rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const float* ys, const int32_t* slot, const float* weight, int64_t tokens,
+                               int32_t top_k, int64_t cols, int64_t rows, const float* base, void* y, bool y_bf16,
+                               hipStream_t s) {
+  const dim3 grid(token_blocks(tokens), (unsigned)((cols + 1023) / 1024));
+  if (y_bf16)
+    hipLaunchKernelGGL(combine_kernel<true>, grid, dim3(256), 0, s, ys, slot, weight, tokens, (int)top_k, cols,
+                       (uint32_t)rows, base, y);
+  else
+    hipLaunchKernelGGL(combine_kernel<false>, grid, dim3(256), 0, s, ys, slot, weight, tokens, (int)top_k, cols,
+                       (uint32_t)rows, base, y);
+  return hipGetLastError();
+}
+
+}  // namespace uw

@@ -1349,6 +1349,139 @@ uw_status uw_grouped_matmul(const uw_handle* experts, int32_t n, const uint16_t*
   return flush();
 }
 
+namespace {
+
+// The parts of uw_moe_forward's workspace; n = tokens * top_k entries.
+struct MoeParts {
+  size_t experts, weights, offsets, order, slot, group, xs, g, u, h, ys, total;
+};
+MoeParts moe_parts(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k) {
+  const size_t n = size_t(tokens) * top_k;
+  MoeParts p;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  p.experts = take(n * 4);
+  p.weights = take(n * 4);
+  p.offsets = take(size_t(experts + 1) * 4);
+  p.order = take(n * 4);
+  p.slot = take(n * 4);
+  p.group = take(uw_group_rows_workspace_bytes(int64_t(n), experts));
+  p.xs = take(n * hidden * 2);
+  p.g = take(n * inter * 4);
+  p.u = take(n * inter * 4);
+  p.h = take(n * inter * 2);
+  p.ys = take(n * hidden * 4);
+  p.total = at;
+  return p;
+}
+
+uw_status moe_impl(const uw_handle* handles, const int32_t* pipelines, const void* logits, int32_t type, int64_t ld,
+                   const float* bias, const uw_route_config* c, const uint16_t* x, const float* base, float* y,
+                   int64_t tokens, void* work, size_t work_bytes) {
+  if (!handles || !pipelines || !logits || !c || !x || !y || !work) return fail(UW_ERR_INVALID_ARG, "null argument");
+  // the workspace stands in for the route's outputs
+  uint8_t* m = static_cast<uint8_t*>(work);
+  if (reinterpret_cast<uintptr_t>(m) % 256) return fail(UW_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+  if (tokens < 1 || tokens > (int64_t(1) << 24)) return fail(UW_ERR_INVALID_ARG, "tokens out of range");
+  if (c->experts < 1 || c->experts > 1024 || c->top_k < 1 || c->top_k > c->experts || c->top_k > 64)
+    return fail(UW_ERR_INVALID_ARG, "experts must be 1..1024, top_k 1..64 and at most the experts");
+  const int32_t ne = c->experts;
+  for (int32_t i = 0; i < ne * 3; ++i)
+    if (!handles[i]) return fail(UW_ERR_INVALID_ARG, "null handle %d", i);
+  const int64_t inter = handles[0]->rows, hidden = handles[0]->cols;
+  hipStream_t main = handles[0]->main;
+  std::vector<uw_handle> part[3];
+  for (int32_t e = 0; e < ne; ++e)
+    for (int j = 0; j < 3; ++j) {
+      const uw_handle h = handles[3 * e + j];
+      if (h->rows != (j < 2 ? inter : hidden) || h->cols != (j < 2 ? hidden : inter))
+        return fail(UW_ERR_SHAPE, "expert %d: gate/up [inter, hidden] and down [hidden, inter] shapes disagree", e);
+      if (h->host_only) return fail(UW_ERR_UNSUPPORTED, "expert %d is not on the device", e);
+      if (h->main != main) return fail(UW_ERR_INVALID_ARG, "all handles must share one main stream (expert %d differs)", e);
+      part[j].push_back(h);
+    }
+  const size_t need = uw_moe_workspace_bytes(tokens, hidden, inter, ne, c->top_k);
+  if (work_bytes < need)
+    return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, %lld tokens need %zu", work_bytes, (long long)tokens, need);
+  const MoeParts p = moe_parts(tokens, hidden, inter, ne, c->top_k);
+  int32_t* experts = reinterpret_cast<int32_t*>(m + p.experts);
+  float* weights = reinterpret_cast<float*>(m + p.weights);
+  int32_t* offsets = reinterpret_cast<int32_t*>(m + p.offsets);
+  int32_t* slot = reinterpret_cast<int32_t*>(m + p.slot);
+  uint16_t* xs = reinterpret_cast<uint16_t*>(m + p.xs);
+  float* g = reinterpret_cast<float*>(m + p.g);
+  float* u = reinterpret_cast<float*>(m + p.u);
+  uint16_t* hh = reinterpret_cast<uint16_t*>(m + p.h);
+  float* ys = reinterpret_cast<float*>(m + p.ys);
+  uw_status st = uw::route_check(logits, type, ld, tokens, bias, c, experts, weights);
+  if (st != UW_OK) return st;
+  const int64_t n = tokens * c->top_k;
+  if (n > (int64_t(1) << 30)) return fail(UW_ERR_INVALID_ARG, "tokens * top_k too large");
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y),
+                  ba = reinterpret_cast<uintptr_t>(base), wa = reinterpret_cast<uintptr_t>(m);
+  const size_t xb = size_t(tokens) * hidden * 2, yb = size_t(tokens) * hidden * 4;
+  if (xa % 16 || ya % 16 || ba % 16) return fail(UW_ERR_INVALID_ARG, "x, base and y must be 16-byte aligned");
+  auto meet = [](uintptr_t a, size_t na, uintptr_t b, size_t nb) { return a < b + nb && b < a + na; };
+  if (meet(xa, xb, ya, yb) || meet(wa, need, ya, yb) || meet(wa, need, xa, xb) ||
+      (base && (meet(wa, need, ba, yb) || (base != y && meet(ba, yb, ya, yb)))))
+    return fail(UW_ERR_INVALID_ARG, "x, base, y and the workspace overlap (base may be y itself)");
+  for (int j = 0; j < 3; ++j)
+    for (int32_t e = 0; e < ne; ++e) {
+      // one row stands in for the expert's share, which routing decides
+      int pl = 0;
+      uw::Variant v;
+      if ((st = matmul_check(part[j][e], x, y, 1, pipelines[j], &pl, &v)) != UW_OK) return st;
+    }
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  UW_HIP(hipStreamIsCapturing(main, &cap));
+  if (cap != hipStreamCaptureStatusNone)
+    return fail(UW_ERR_UNSUPPORTED, "the layer waits for its group sizes and cannot be captured into a graph");
+  if ((st = uw::route_launch(logits, type, ld, tokens, bias, c, experts, weights, main)) != UW_OK ||
+      (st = uw_group_rows(experts, n, ne, offsets, reinterpret_cast<int32_t*>(m + p.order), slot, m + p.group,
+                          p.xs - p.group, main)) != UW_OK)
+    return st;
+  std::vector<int32_t> host(ne + 1);
+  UW_HIP(hipMemcpyAsync(host.data(), offsets, size_t(ne + 1) * 4, hipMemcpyDeviceToHost, main));
+  // the copy of the activations needs no host: it runs while the host waits
+  st = uw_dispatch_rows(x, hidden, slot, tokens, c->top_k, hidden, xs, n, main);
+  UW_HIP(hipStreamSynchronize(main));  // also on failure: the copy writes `host`
+  if (st != UW_OK) return st;
+  const int64_t rows = host[ne];
+  if (rows > 0) {
+    const std::vector<int64_t> offs(host.begin(), host.end());
+    if ((st = uw_grouped_matmul(part[0].data(), ne, xs, offs.data(), g, pipelines[0])) != UW_OK ||
+        (st = uw_grouped_matmul(part[1].data(), ne, xs, offs.data(), u, pipelines[1])) != UW_OK)
+      return st;
+    UW_HIP(uw::launch_silu_mul(g, u, hh, rows * inter, main));
+    if ((st = uw_grouped_matmul(part[2].data(), ne, hh, offs.data(), ys, pipelines[2])) != UW_OK) return st;
+  }
+  return uw_combine_rows(ys, n, slot, weights, tokens, c->top_k, hidden, base, y, UW_F32, main);
+}
+
+}  // namespace
+
+size_t uw_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k) {
+  if (tokens < 1 || tokens > (int64_t(1) << 24) || hidden < 1 || inter < 1 || hidden > (int64_t(1) << 24) ||
+      inter > (int64_t(1) << 24) || experts < 1 || experts > 1024 || top_k < 1 || top_k > experts || top_k > 64)
+    return 0;
+  return moe_parts(tokens, hidden, inter, experts, top_k).total;
+}
+
+uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, const void* logits_dev, int32_t type,
+                         int64_t ld, const float* bias_dev, const uw_route_config* config, const uint16_t* x_dev,
+                         const float* base_dev, float* y_dev, int64_t tokens, void* work_dev, size_t work_bytes) {
+  try {
+    return moe_impl(handles, pipelines, logits_dev, type, ld, bias_dev, config, x_dev, base_dev, y_dev, tokens,
+                    work_dev, work_bytes);
+  } catch (const std::bad_alloc&) {
+    return fail(UW_ERR_OOM, "host allocation failed");
+  }
+}
+
 void uw_free(uw_handle h) {
   if (!h) return;
   if (h->pinned) {

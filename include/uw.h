@@ -319,6 +319,156 @@ uw_status uw_stack_forward(const uw_handle* handles, const int32_t* pipelines, i
                            void* work_dev, size_t work_bytes);
 size_t uw_stack_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter);
 
+/* ---- Routing of tokens to experts, and back ----
+ *
+ * uw_route chooses each token's experts, uw_group_rows sorts the (token,
+ * choice) entries by expert, uw_dispatch_rows copies the activations to their
+ * experts' rows (uw_grouped_matmul's X), and uw_combine_rows sums the experts'
+ * output rows back per token.  uw_moe_forward runs a layer of SwiGLU experts
+ * through all of them.  These calls only launch kernels on `stream` (NULL =
+ * the null stream), allocate nothing and can be captured into a graph, except
+ * uw_moe_forward.  All pointers are device memory of the current device.
+ * Buffers must not overlap, except where said.  0 < tokens <= 2^24 and
+ * tokens * top_k <= 2^30, else UW_ERR_INVALID_ARG. */
+
+typedef enum { UW_F32 = 0, UW_BF16 = 1 } uw_type;
+typedef enum { UW_SCORE_SOFTMAX = 0, UW_SCORE_SIGMOID = 1 } uw_score;
+typedef enum { UW_GROUP_MAX = 0, UW_GROUP_TOP2 = 1 } uw_group_score;
+
+typedef struct {
+  int32_t experts;      /* 1..1024                                              */
+  int32_t top_k;        /* choices per token: 1..64, at most experts            */
+  int32_t score;        /* uw_score                                             */
+  int32_t groups;       /* groups of experts/groups consecutive experts: 1..64,
+                           a divisor of experts; 1 = no groups                  */
+  int32_t top_groups;   /* groups kept per token: 1..groups                     */
+  int32_t group_score;  /* uw_group_score: a group's merit                      */
+  int32_t renormalise;  /* nonzero: weights are divided by their sum            */
+  float scale;          /* finite factor on the weights                         */
+} uw_route_config;
+
+/* With a token's logits l: score s = softmax(l) over all experts, or 1 / (1 +
+ * exp(-l)).  Choice c = s + bias, or l itself without a bias (bias_dev NULL:
+ * the scores' order is the logits').  The top_groups groups of greatest merit
+ * stay -- UW_GROUP_MAX: their largest c, UW_GROUP_TOP2: the sum of their two
+ * largest s + bias (the largest alone in a group of one) -- and of their
+ * experts the top_k of largest c, in descending order.  Equal values go to the
+ * lower index.  Scores that decide are computed and compared in 64 bits.
+ * weight = s of the chosen (never the bias), divided by the sum over the
+ * chosen if renormalise (a sum of 0 leaves zeros), times scale.
+ * An expert is no candidate where its logit is -inf or NaN, or its c is -inf
+ * or NaN (a bias of -inf switches it off for all tokens); its score is 0.  A
+ * logit of +inf counts as the largest finite value.  Choices that a token has
+ * no candidates left for get expert -1 and weight 0.
+ * logits_dev: [tokens, experts] of `type` (UW_F32 or UW_BF16), row stride ld
+ * elements (ld >= experts); bias_dev: float [experts] or NULL; experts_dev
+ * [tokens, top_k] int32 and weights_dev [tokens, top_k] float receive the
+ * choices. */
+uw_status uw_route(const void* logits_dev, int32_t type, int64_t ld, int64_t tokens, const float* bias_dev,
+                   const uw_route_config* config, int32_t* experts_dev, float* weights_dev, void* stream);
+
+/* Stable counting sort of n entries by index_dev[i] in [0, groups); entries
+ * with any other index are ungrouped.  offsets_dev [groups + 1]: group g has
+ * positions offsets[g] .. offsets[g+1]-1 (offsets[groups] = grouped entries).
+ * order_dev [n]: the entry at each position, equal groups in entry order, the
+ * ungrouped entries behind the last group.  slot_dev [n]: each entry's
+ * position, -1 for an ungrouped one.  The result does not depend on timing.
+ * 1 <= n <= 2^30, 1 <= groups <= 4000.  work_dev: at least
+ * uw_group_rows_workspace_bytes(n, groups) bytes (may be NULL where that is 0;
+ * the size is 0 for arguments out of range).  A workspace belongs to one call
+ * at a time. */
+size_t uw_group_rows_workspace_bytes(int64_t n, int32_t groups);
+uw_status uw_group_rows(const int32_t* index_dev, int64_t n, int32_t groups, int32_t* offsets_dev, int32_t* order_dev,
+                        int32_t* slot_dev, void* work_dev, size_t work_bytes, void* stream);
+
+/* xs[slot[t * top_k + j]] = x[t] for every entry whose slot is in [0, rows);
+ * other entries are skipped and rows of xs that no entry names keep their
+ * contents.  x_dev: bf16 [tokens, cols], row stride ldx (a multiple of 8, >=
+ * cols); xs_dev: bf16 [rows, cols]; cols a multiple of 8; both 16-byte aligned.
+ * No two entries may name one row. */
+uw_status uw_dispatch_rows(const uint16_t* x_dev, int64_t ldx, const int32_t* slot_dev, int64_t tokens, int32_t top_k,
+                           int64_t cols, uint16_t* xs_dev, int64_t rows, void* stream);
+
+/* y[t] = base[t] + sum over j of weights[t * top_k + j] * ys[slot[t * top_k + j]],
+ * summed in float32 in the order of j; entries whose slot is outside [0, rows)
+ * are left out and their rows not read.  ys_dev: float [rows, cols]; base_dev:
+ * float [tokens, cols] or NULL (zeros); y_dev: [tokens, cols] of y_type
+ * (UW_F32, or UW_BF16 rounded to nearest even once); a float y may be base
+ * itself.  cols a multiple of 8; ys, base and y 16-byte aligned. */
+uw_status uw_combine_rows(const float* ys_dev, int64_t rows, const int32_t* slot_dev, const float* weights_dev,
+                          int64_t tokens, int32_t top_k, int64_t cols, const float* base_dev, void* y_dev,
+                          int32_t y_type, void* stream);
+
+/* One mixture-of-experts layer: y[t] = base[t] + sum over the token's chosen
+ * experts e of weight_e * down_e(silu(gate_e x[t]) * up_e x[t]).
+ * handles[3e .. 3e+2] are expert e's gate, up ([inter, hidden]) and down
+ * ([hidden, inter]), experts = config->experts of them, one shape, all on the
+ * device and with one main stream, on which everything runs.  pipelines[3] is
+ * used as in uw_mlp_forward for all experts.  logits, ld, bias and config as
+ * in uw_route; x_dev bf16 [tokens, hidden]; base_dev float [tokens, hidden] or
+ * NULL, may be y; y_dev float [tokens, hidden].  work_dev: 256-byte aligned,
+ * uw_moe_workspace_bytes bytes (0 for arguments out of range).  The experts'
+ * products need the group sizes on the host: the call waits for the main
+ * stream once, after routing, and is refused (UW_ERR_UNSUPPORTED) while that
+ * stream is being captured.  Products with more than 2^24 rows, or over
+ * uw_matmul's limits, are refused as there. */
+size_t uw_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k);
+uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, const void* logits_dev, int32_t type,
+                         int64_t ld, const float* bias_dev, const uw_route_config* config, const uint16_t* x_dev,
+                         const float* base_dev, float* y_dev, int64_t tokens, void* work_dev, size_t work_bytes);
+
+/* ---- Low-rank adapters of many requests beside a shared projection ----
+ *
+ * A uw_lora holds the adapters of one projection W [rows, cols] in numbered
+ * slots on the device that was current when it was made: slot i's A [rank,
+ * cols] and B [rows, rank], bf16, and a factor.  uw_lora_plan sorts a batch's
+ * tokens by slot once; uw_lora_apply then adds, for any projection of any
+ * layer, y[t] = base[t] + scale_i * B_i (A_i x[t]) for the token's slot i, on
+ * top of uw_matmul's output.  Products accumulate in float32 and A_i x[t] is
+ * never rounded below it.  The calls run on `stream` and except create and
+ * free only launch kernels, so they can be captured. */
+typedef struct uw_adapters* uw_lora;
+#define UW_LORA_MAX_RANK 256
+
+/* rows a multiple of 16, cols of 64 (at most 2^23 each), 1..4000 slots of up to
+ * max_rank ranks (1..UW_LORA_MAX_RANK).  All slots start empty (rank 0: no
+ * adapter).  Device memory: slots * max_rank (rounded up to 16) * (rows +
+ * cols) * 2 bytes. */
+uw_status uw_lora_create(int64_t rows, int64_t cols, int32_t slots, int32_t max_rank, uw_lora* out);
+/* Copy an adapter into a slot, replacing what it held: a_dev [rank, cols] and
+ * b_dev [rows, rank], contiguous bf16; 0 <= rank <= max_rank (0 empties the
+ * slot, the pointers are not read).  The sources may be changed once the
+ * stream has run the copy.  Calls on other streams that use the slot must be
+ * ordered by the caller. */
+uw_status uw_lora_load(uw_lora h, int32_t slot, const uint16_t* a_dev, const uint16_t* b_dev, int32_t rank, float scale,
+                       void* stream);
+void uw_lora_free(uw_lora h);
+
+/* Sort a batch: slot_dev [tokens] int32 is each token's slot; any value
+ * outside [0, slots) means no adapter.  plan_dev (16-byte aligned,
+ * uw_lora_plan_bytes(tokens, slots) bytes; 0 for arguments out of range) holds
+ * the result for any number of uw_lora_apply calls with the same tokens and
+ * slots; a plan made for other numbers makes uw_lora_apply leave y as it is. */
+size_t uw_lora_plan_bytes(int64_t tokens, int32_t slots);
+uw_status uw_lora_plan(const int32_t* slot_dev, int64_t tokens, int32_t slots, void* plan_dev, size_t plan_bytes,
+                       void* stream);
+
+/* y_i[t] = base_i[t] + scale * B (A x[t]) for n projections (1..4) that read the
+ * same x, e.g. gate and up: adapters[i] with one number of cols and slots.
+ * x_dev: bf16 [tokens, cols], row stride ldx (>= cols, a multiple of 8);
+ * bases_dev: NULL or n pointers, a NULL one meaning zeros, float [tokens, rows]
+ * with row strides ldbase; ys_dev: n float outputs with row strides ldy (>=
+ * rows, multiples of 4); all 16-byte aligned.  base_i may be y_i with the same
+ * stride (in place: uw_matmul's output).  Tokens without an adapter get their
+ * base.  work_dev: 256-byte aligned, at least uw_lora_workspace_bytes bytes;
+ * calls that overlap in time must not share it.  UW_ERR_INVALID_ARG if the
+ * current device is not the adapters'. */
+size_t uw_lora_workspace_bytes(const uw_lora* adapters, int32_t n, int64_t tokens);
+uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev, size_t plan_bytes,
+                        const uint16_t* x_dev, int64_t ldx, const float* const* bases_dev, const int64_t* ldbase,
+                        float* const* ys_dev, const int64_t* ldy, int64_t tokens, void* work_dev, size_t work_bytes,
+                        void* stream);
+
 /* ---- Streams with a CU mask (section 九's decode/compute split) ---- */
 
 /* Create a stream limited to compute units [cu_first, cu_first + cu_count)

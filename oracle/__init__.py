@@ -37,6 +37,7 @@ from .gemm import (  # noqa: F401
     bf16_to_f64, f64_to_bf16_rne, matmul_fp64, matmul_fp64_rows, silu_mul_bf16,
     mlp_layer_fp64, rel_err,
 )
+from . import routing  # noqa: F401
 
 # Every oracle function and what pins it (tests/test_oracle_*.py).  None is
 # "parity unpinned".
@@ -54,5 +55,8 @@ PARITY = {
     "silu_mul_bf16": "closed-form values; RNE ties by hand",
     "write_bundle/read_bundle": "round trip to the original weights; byte-equal to the library's own writer "
                                 "(an independent implementation of the same layout); header fields by struct",
+    "routing.route": "hand-worked choices; weights against scipy's softmax and expit; group choices by brute force",
+    "routing.group_rows/dispatch_rows/combine_rows": "hand-worked case; round trip through unit weights",
+    "routing.lora": "exact rational sums; the merged weight W + scale B A",
     "transcode_bundle": "equals palette_encode of the original weights (the Huffman round trip is exact)",
 }
