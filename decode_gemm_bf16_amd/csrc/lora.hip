@@ -13,6 +13,8 @@
 //           bf16 B are exact in float32, so that nothing is rounded to bf16.
 // What bounds it: few tokens, the adapters' bytes; many, base and y (8 bytes
 // an output element against 2 * rank bf16 operations).
+#include <type_traits>
+
 #include "recon.h"
 #include "routing.h"
 
@@ -21,69 +23,104 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kSub = kPlanTile / 16;  // 16-token subtiles of a tile
-constexpr int kRankBlock = 64;        // ranks per shrink workgroup
+constexpr int kRankBlock = 64;        // ranks per shrink workgroup and per staging of v
+constexpr int kShrinkWaves = 8;
+
+__device__ __forceinline__ bool plan_has(const LoraArgs& a, int tile) {
+  return a.header->tokens == a.tokens && a.header->slots == a.slots && tile < a.header->tiles;
+}
 
 // ---- shrink ----
 //
-// One workgroup: one tile, up to 64 ranks, one of ksplit parts of cols.  Its 4
-// waves take every fourth 32-column step; each holds all 16 x 16 blocks of
-// the tile (4 x 4), so that a step's loads (16 bytes a lane) feed 16 matrix
-// instructions.  The waves' sums are added in LDS.
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
-  __shared__ float red[4][16][kRankBlock + 1];
-  const LoraProj& p = a.proj[blockIdx.z % a.nproj];
-  const int rblock = blockIdx.z / a.nproj;
-  if (a.header->tokens != a.tokens || a.header->slots != a.slots || (int)blockIdx.x >= a.header->tiles) return;
-  const PlanTile tile = a.tiles[blockIdx.x];
-  if (tile.slot < 0) return;
-  const int rank = p.table[tile.slot].rank - rblock * kRankBlock;
-  if (rank <= 0) return;
-  const int nr = rank >= kRankBlock ? kRankBlock / 16 : (rank + 15) / 16;
-  const int ns = (tile.len + 15) / 16;
+// One workgroup: half a tile (32 tokens from i0 on), up to 64 ranks, one of
+// ksplit parts of cols, which its 8 waves divide among them in 32-column steps.
+// A lies in the order of the operands (1 KB for 16 ranks x 32 columns);
+// a wave holds all NS x NR blocks of 16 tokens x 16 ranks, so that a step's
+// NS + NR loads of 16 bytes a lane feed NS * NR matrix instructions, and U steps'
+// loads are in flight at once.  The waves' sums are added in LDS.
+template <int NS, int NR, int U>
+__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int i0,
+                                            int kpart, int rblock, int nr, float (&red)[kShrinkWaves][16][kRankBlock]) {
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int steps = a.cols / 32, per = (steps + a.ksplit - 1) / a.ksplit;
-  const int s0 = blockIdx.y * per, s1 = s0 + per < steps ? s0 + per : steps;
-  const uint16_t* ar = p.a + ((int64_t)tile.slot * p.rank16 + rblock * kRankBlock + r) * a.cols + q * 8;
-  const uint16_t* xr[kSub];
+  const int steps = a.cols / 32, parts = a.ksplit * kShrinkWaves, part = kpart * kShrinkWaves + w;
+  const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
+  const uint16_t* ar[NR];
+  const uint16_t* xr[NS];
 #pragma unroll
-  for (int i = 0; i < kSub; ++i) {
-    const int k = i * 16 + r;  // rows past the tile's end read its first row; they are not stored
-    xr[i] = a.x + (int64_t)a.order[tile.start + (k < tile.len ? k : 0)] * a.ldx + q * 8;
+  for (int j = 0; j < NR; ++j)  // blocks past the adapter's ranks repeat the first; they are not stored
+    ar[j] = p.a + ((int64_t)tile.slot * p.rank16 + rblock * kRankBlock + (j < nr ? j : 0) * 16) * a.cols + lane * 8;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int k = i0 + i * 16 + r;  // rows past the tile's end repeat its last
+    xr[i] = a.x + (int64_t)a.order[tile.start + (k < tile.len ? k : tile.len - 1)] * a.ldx + q * 8;
   }
-  f32x4 acc[kSub][4] = {};
-  for (int s = s0 + w; s < s1; s += 4) {
-    bf16x8 xv[kSub], av[4];
+  f32x4 acc[NS][NR] = {};
+  for (int s = s0; s < s1; s += U) {
+    bf16x8 xv[U][NS], av[U][NR];
 #pragma unroll
-    for (int i = 0; i < kSub; ++i)
-      if (i < ns) xv[i] = *(const bf16x8*)(xr[i] + s * 32);
+    for (int u = 0; u < U; ++u) {  // steps past the last repeat the batch's first
+      const int64_t at = s + u < s1 ? s + u : s;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < nr) av[j] = *(const bf16x8*)(ar + (int64_t)j * 16 * a.cols + s * 32);
+      for (int j = 0; j < NR; ++j) av[u][j] = *(const bf16x8*)(ar[j] + at * 512);
 #pragma unroll
-    for (int i = 0; i < kSub; ++i)
+      for (int i = 0; i < NS; ++i) xv[u][i] = *(const bf16x8*)(xr[i] + at * 32);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all loads in flight before the first product
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i < ns && j < nr) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[i], av[j], acc[i][j], 0, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      if (s + u >= s1) break;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[u][i], av[u][j], acc[i][j], 0, 0, 0);
+    }
   }
   // block (i, j): token 4 q + k of subtile i, rank 16 j + r
-  float* out = p.part + ((int64_t)blockIdx.y * a.tokens + tile.start) * p.rank16 + rblock * kRankBlock;
-  const int ranks = nr * 16;
+  float* out = p.part + ((int64_t)kpart * a.tokens + tile.start + i0) * p.rank16 + rblock * kRankBlock;
 #pragma unroll
-  for (int i = 0; i < kSub; ++i) {
-    if (i >= ns) break;
-    __syncthreads();
+  for (int i = 0; i < NS; ++i) {
+    if (i) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) red[w][4 * q + k][16 * j + r] = acc[i][j][k];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * ranks; e += 256) {
-      const int tk = e / ranks, rk = e - tk * ranks;
-      if (i * 16 + tk < tile.len)
-        out[(int64_t)(i * 16 + tk) * p.rank16 + rk] =
-            (red[0][tk][rk] + red[1][tk][rk]) + (red[2][tk][rk] + red[3][tk][rk]);
+    const int rk = threadIdx.x % (NR * 16);
+    for (int tk = threadIdx.x / (NR * 16); tk < 16 && i0 + i * 16 + tk < tile.len; tk += 64 * kShrinkWaves / (NR * 16)) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kShrinkWaves; ++k) v += red[k][tk][rk];
+      if (rk < nr * 16) out[(int64_t)(i * 16 + tk) * p.rank16 + rk] = v;
     }
+  }
+}
+
+__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_shrink_kernel(LoraArgs a) {
+  __shared__ float red[kShrinkWaves][16][kRankBlock];
+  const LoraProj& p = a.proj[blockIdx.z % a.nproj];
+  const int rblock = blockIdx.z / a.nproj;
+  const int half = blockIdx.x / a.ksplit, kpart = blockIdx.x - half * a.ksplit, i0 = (half & 1) * 32;
+  if (!plan_has(a, half >> 1)) return;
+  const PlanTile tile = a.tiles[half >> 1];
+  if (tile.slot < 0 || i0 >= tile.len) return;
+  const int rank = p.table[tile.slot].rank - rblock * kRankBlock;
+  if (rank <= 0) return;
+  const int nr = rank >= kRankBlock ? kRankBlock / 16 : (rank + 15) / 16;
+  if (tile.len - i0 <= 16) {
+    if (nr == 1)
+      shrink_tile<1, 1, 4>(a, p, tile, i0, kpart, rblock, nr, red);
+    else if (nr == 2)
+      shrink_tile<1, 2, 4>(a, p, tile, i0, kpart, rblock, nr, red);
+    else
+      shrink_tile<1, 4, 3>(a, p, tile, i0, kpart, rblock, nr, red);
+  } else {
+    if (nr == 1)
+      shrink_tile<2, 1, 4>(a, p, tile, i0, kpart, rblock, nr, red);
+    else if (nr == 2)
+      shrink_tile<2, 2, 3>(a, p, tile, i0, kpart, rblock, nr, red);
+    else
+      shrink_tile<2, 4, 2>(a, p, tile, i0, kpart, rblock, nr, red);
   }
 }
 
@@ -100,76 +137,161 @@ __device__ __forceinline__ uint16_t bf16_part(float& v) {
   return (uint16_t)(u >> 16);
 }
 
-// One workgroup: one tile, 256 rows of B, 64 per wave.  B is the A operand (16
-// rows x 16 ranks), so that a lane's 4 results are 4 neighbouring columns of
-// one token's y.
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a) {
-  // scale * v in three bf16 parts: [part][token][rank], one 16-rank block at a time
-  __shared__ __attribute__((aligned(16))) uint16_t parts[3][kPlanTile][16 + 4];
-  const LoraProj& p = a.proj[blockIdx.z];
-  if (a.header->tokens != a.tokens || a.header->slots != a.slots || (int)blockIdx.x >= a.header->tiles) return;
-  if ((int)blockIdx.y * 256 >= p.rows) return;
-  const PlanTile tile = a.tiles[blockIdx.x];
-  const LoraSlot entry = tile.slot >= 0 ? p.table[tile.slot] : LoraSlot{0, 0.f};
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.y * 256 + w * 64;
-  const int nr = (entry.rank + 15) / 16, ns = (tile.len + 15) / 16;
-  if (nr == 0 && p.base == p.y && p.ldbase == p.ldy) return;  // in place, nothing to add
-  f32x4 acc[kSub][4];
-  int64_t tok[kSub];
+// scale * v in three bf16 parts: [part][token][rank]; 8 ranks of padding keep
+// the lanes' 8-byte reads of 16 tokens apart in the banks
+typedef uint16_t LoraParts[3][kPlanTile][kRankBlock + 8];
+
+// Thread t of 256: token t / 4, ranks 4 (t % 4) .. + 3 of each 16-rank block.
+__device__ __forceinline__ void stage_parts(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int rank,
+                                            float scale, int r0, int blocks, LoraParts& parts) {
+  const int k = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
+  if (k >= tile.len) return;
+  const float* src = p.part + (int64_t)(tile.start + k) * p.rank16 + r0 + c;
+  const int64_t next = (int64_t)a.tokens * p.rank16;
+  f32x4 v[kRankBlock / 16] = {};
+  for (int s = 0; s < a.ksplit; ++s) {
 #pragma unroll
-  for (int i = 0; i < kSub; ++i) {
-    const int k = i * 16 + r;
-    tok[i] = k < tile.len ? a.order[tile.start + k] : -1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 16 * j + 4 * q;
-      acc[i][j] = p.base && tok[i] >= 0 && n < p.rows ? *(const f32x4*)(p.base + tok[i] * p.ldbase + n)
-                                                      : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int i = 0; i < kRankBlock / 16; ++i)  // blocks past the last repeat it
+      v[i] += *(const f32x4*)(src + s * next + (i < blocks ? i : blocks - 1) * 16);
   }
-  const uint16_t* b = p.b + (int64_t)(tile.slot < 0 ? 0 : tile.slot) * p.rank16 * p.rows;
-  for (int rb = 0; rb < nr; ++rb) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < 16 * tile.len; e += 256) {
-      const int k = e >> 4, c = e & 15;
-      const float* src = p.part + (int64_t)(tile.start + k) * p.rank16 + rb * 16 + c;
-      float v = 0.f;
-      for (int s = 0; s < a.ksplit; ++s) v += src[(int64_t)s * a.tokens * p.rank16];
-      // ranks past the adapter's own: an infinity in x makes NaN of them
-      v = rb * 16 + c < entry.rank ? v * entry.scale : 0.f;
-      parts[0][k][c] = bf16_part(v);
-      parts[1][k][c] = bf16_part(v);
-      parts[2][k][c] = bf16_part(v);
-    }
-    __syncthreads();
-    s16x4 bv[4];
+#pragma unroll
+  for (int i = 0; i < kRankBlock / 16; ++i) {
+    if (i >= blocks) break;
+    uint16_t h[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 16 * j + r;
-      bv[j] = n < p.rows ? *(const s16x4*)(b + ((int64_t)rb * p.rows + n) * 16 + 4 * q) : s16x4{0, 0, 0, 0};
+      // ranks past the adapter's own: an infinity in x makes NaN of them
+      float f = r0 + i * 16 + c + j < rank ? v[i][j] * scale : 0.f;
+#pragma unroll
+      for (int m = 0; m < 3; ++m) h[m][j] = bf16_part(f);
     }
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      if (i >= ns) break;
+    for (int m = 0; m < 3; ++m)
+      *(u32x2*)&parts[m][k][i * 16 + c] =
+          u32x2{h[m][0] | (uint32_t)h[m][1] << 16, h[m][2] | (uint32_t)h[m][3] << 16};
+  }
+}
+
+// One workgroup: one tile; each of its 4 waves takes C groups of 64 rows of B
+// (every fourth one) at once, `reps` times over, and 16 NS tokens at a time.  v is
+// the A operand (16 tokens x 16 ranks) and B the B operand; row 4 r + j of a
+// group is column r of its j-th 16-column product, so that a lane's results of
+// the four products are 4 neighbouring columns of y, and a load or store of 16
+// bytes a lane covers 256 bytes of each of 4 tokens.  Row 4 q + k of the A operand
+// is token q + 4 k of 16, so that up to 4 KM tokens take the first KM of a lane's
+// 4 results.  B lies in the order of the operands: a lane's 4 x 4 values of a
+// group and rank block are 32 bytes.
+template <int NS, int KM, int C>
+__device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int reps,
+                                            LoraParts& parts) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int groups = (p.rows + 63) / 64;
+  const uint16_t* b = p.b + (int64_t)(tile.slot < 0 ? 0 : tile.slot) * p.rank16 * groups * 64 + lane * 16;
+  const LoraSlot entry = tile.slot >= 0 ? p.table[tile.slot] : LoraSlot{0, 0.f};
+  if (entry.rank == 0 && p.base == p.y && p.ldbase == p.ldy) return;  // in place, nothing to add
+  const int nr = (entry.rank + 15) / 16;
+  for (int rep = 0; rep < reps; ++rep)
+    for (int i0 = 0; i0 < tile.len; i0 += 16 * NS) {
+      const int g0 = (blockIdx.x * reps + rep) * 4 * C + w;
+      int tok[NS][KM];
 #pragma unroll
-      for (int h = 2; h >= 0; --h) {  // the smallest part first
-        // tokens past the tile's end: stale LDS, in columns of the result that are not stored
-        const s16x4 vv = *(const s16x4*)&parts[h][i * 16 + r][4 * q];
+      for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bv[j], vv, acc[i][j], 0, 0, 0);
+        for (int k = 0; k < KM; ++k) {
+          const int t = i0 + i * 16 + q + 4 * k;  // past the tile's end: its last token, not stored
+          tok[i][k] = a.order[tile.start + (t < tile.len ? t : tile.len - 1)];
+        }
+      u32x4 bv[C][2];
+      auto load_b = [&](int rb) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int g = g0 + 4 * c < groups ? g0 + 4 * c : groups - 1;
+          const u32x4* src = (const u32x4*)(b + ((int64_t)rb * groups + g) * 1024);
+          bv[c][0] = src[0];
+          bv[c][1] = src[1];
+        }
+      };
+      if (nr > 0) load_b(0);
+      f32x4 acc[C][NS][4] = {};
+      if (p.base) {
+        // columns past the last row of B read the last four: no branch between the loads
+        f32x4 v[C][NS][KM];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int n = (g0 + 4 * c) * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4;
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int k = 0; k < KM; ++k) v[c][i][k] = *(const f32x4*)(p.base + (int64_t)tok[i][k] * p.ldbase + nc);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int k = 0; k < KM; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[c][i][j][k] = v[c][i][k][j];
+      }
+      for (int r0 = 0; r0 < nr; r0 += kRankBlock / 16) {
+        const int blocks = nr - r0 < kRankBlock / 16 ? nr - r0 : kRankBlock / 16;
+        if ((rep == 0 && i0 == 0) || nr > kRankBlock / 16) {  // else the parts of all ranks are there
+          if (rep || i0 || r0) __syncthreads();
+          stage_parts(a, p, tile, entry.rank, entry.scale, r0 * 16, blocks, parts);
+          __syncthreads();
+        }
+        for (int rb = 0; rb < blocks; ++rb) {
+          s16x4 now[C][4];
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              now[c][j] = __builtin_bit_cast(s16x4, u32x2{bv[c][j >> 1][(j & 1) * 2], bv[c][j >> 1][(j & 1) * 2 + 1]});
+          if (r0 + rb + 1 < nr) load_b(r0 + rb + 1);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+#pragma unroll
+            for (int h = 2; h >= 0; --h) {  // the smallest part first
+              // tokens past the tile's end: stale LDS, in rows of the result that are not stored
+              const s16x4 vv = *(const s16x4*)&parts[h][i0 + i * 16 + (r >> 2) + 4 * (r & 3)][rb * 16 + 4 * q];
+#pragma unroll
+              for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  acc[c][i][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vv, now[c][j], acc[c][i][j], 0, 0, 0);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int n = (g0 + 4 * c) * 64 + 4 * r;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int k = 0; k < KM; ++k)
+            if (i0 + i * 16 + q + 4 * k < tile.len && n < p.rows)
+              *(f32x4*)(p.y + (int64_t)tok[i][k] * p.ldy + n) =
+                  f32x4{acc[c][i][0][k], acc[c][i][1][k], acc[c][i][2][k], acc[c][i][3][k]};
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kSub; ++i) {
-    if (tok[i] < 0) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 16 * j + 4 * q;
-      if (n < p.rows) *(f32x4*)(p.y + tok[i] * p.ldy + n) = acc[i][j];
-    }
-  }
+}
+
+// C: groups of 64 rows per wave; two at once where the tile has at most 4 tokens.
+template <int C>
+__global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) LoraParts parts;
+  const LoraProj& p = a.proj[blockIdx.z];
+  if (!plan_has(a, blockIdx.y)) return;
+  if ((int)blockIdx.x * 256 * C >= p.rows) return;
+  const PlanTile tile = a.tiles[blockIdx.y];
+  constexpr int kFew = C > 2 ? 2 : C;
+  if (tile.len <= 4)
+    expand_tile<1, 1, kFew>(a, p, tile, C / kFew, parts);
+  else if (C > 1 || tile.len <= 32)
+    expand_tile<2, 4, 1>(a, p, tile, C, parts);
+  else
+    expand_tile<4, 4, 1>(a, p, tile, C, parts);
 }
 
 // ---- loading an adapter into a slot ----
@@ -177,12 +299,19 @@ __global__ __launch_bounds__(256) void lora_load_kernel(const uint16_t* __restri
                                                         int64_t rows, int64_t cols, int rank, float scale,
                                                         uint16_t* __restrict__ a_slot, uint16_t* __restrict__ b_slot,
                                                         LoraSlot* __restrict__ entry) {
-  const int64_t ranks = (rank + 15) / 16 * 16, na = ranks * cols, nb = ranks * rows;
+  const int64_t rows64 = (rows + 63) / 64 * 64, ranks = (rank + 15) / 16 * 16, na = ranks * cols, nb = ranks * rows64;
   const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, stride = (int64_t)gridDim.x * 256;
-  for (int64_t i = first; i < na; i += stride) a_slot[i] = i < rank * cols ? a[i] : 0;
+  for (int64_t i = first; i < na; i += stride) {
+    // [rank / 16][col / 32][q][r][8]: rank r of a block, columns 8 q .. + 7 of a step
+    const int64_t rb = i / (cols * 16), m = i % 512;
+    const int64_t c = rb * 16 + m / 8 % 16, k = i / 512 % (cols / 32) * 32 + m / 128 * 8 + m % 8;
+    a_slot[i] = c < rank ? a[c * cols + k] : 0;
+  }
   for (int64_t i = first; i < nb; i += stride) {
-    const int64_t rb = i / (rows * 16), n = i / 16 % rows, c = rb * 16 + i % 16;
-    b_slot[i] = c < rank ? b[n * rank + c] : 0;
+    // [rank / 16][row / 64][q][r][j][4]: row 4 r + j of a group, ranks 4 q .. + 3 of a block
+    const int64_t rb = i / (rows64 * 16), g = i / 1024 % (rows64 / 64), m = i % 1024;
+    const int64_t n = g * 64 + m / 16 % 16 * 4 + m / 4 % 4, c = rb * 16 + m / 256 * 4 + m % 4;
+    b_slot[i] = c < rank && n < rows ? b[n * rank + c] : 0;
   }
   if (first == 0) *entry = LoraSlot{rank, scale};
 }
@@ -195,10 +324,10 @@ int64_t lora_tiles_max(int64_t tokens, int32_t slots) {
 }
 
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj) {
-  const int64_t blocks = lora_tiles_max(tokens, slots) * nproj, steps = cols / 32;
-  int64_t k = 512 / blocks, most = steps / 16;  // at least 4 steps a wave
-  k = k < most ? k : most;
-  return (int)(k < 1 ? 1 : k > 16 ? 16 : k);
+  const int64_t blocks = (lora_tiles_max(tokens, slots) + tokens / kPlanTile) * nproj, steps = cols / 32;
+  int k = 8;
+  while (k > 1 && (k * blocks > 512 || steps < k * kShrinkWaves)) k /= 2;
+  return k;
 }
 
 hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
@@ -208,8 +337,12 @@ hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
     rows = a.proj[i].rows > rows ? a.proj[i].rows : rows;
   }
   const unsigned rblocks = (rank16 + kRankBlock - 1) / kRankBlock;
-  hipLaunchKernelGGL(lora_shrink_kernel, dim3(a.tiles_max, a.ksplit, rblocks * a.nproj), dim3(256), 0, s, a);
-  hipLaunchKernelGGL(lora_expand_kernel, dim3(a.tiles_max, (rows + 255) / 256, a.nproj), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(lora_shrink_kernel, dim3(2 * a.tiles_max * a.ksplit, 1, rblocks * a.nproj), dim3(64 * kShrinkWaves),
+                     0, s, a);
+  if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
+    hipLaunchKernelGGL(lora_expand_kernel<4>, dim3((rows + 1023) / 1024, a.tiles_max, a.nproj), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(lora_expand_kernel<1>, dim3((rows + 255) / 256, a.tiles_max, a.nproj), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -12,7 +12,7 @@
 #include "runtime_internal.h"
 
 struct uw_adapters {
-  int64_t rows = 0, cols = 0;
+  int64_t rows = 0, cols = 0, rows64 = 0;
   int32_t slots = 0, max_rank = 0, rank16 = 0;
   int device = 0;
   void* mem = nullptr;
@@ -40,6 +40,7 @@ uw_status fail(uw_status st, const char* fmt, ...) {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxEntries = int64_t(1) << 30;
+constexpr int64_t kMaxLoraTokens = int64_t(1) << 20;  // two halves of every tile within a grid dimension
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -65,9 +66,9 @@ bool overlap_rows(const float* p, int64_t pcols, int64_t ldp, const float* q, in
 // Bytes from the first to past the last element of [rows, cols] with row stride ld.
 size_t span(int64_t rows, int64_t cols, int64_t ld, size_t size) { return size_t((rows - 1) * ld + cols) * size; }
 
-uw_status check_tokens(int64_t tokens) {
+uw_status check_tokens(int64_t tokens, int64_t most = kMaxTokens) {
   if (tokens < 1) return fail(UW_ERR_INVALID_ARG, "tokens must be >= 1");
-  if (tokens > kMaxTokens) return fail(UW_ERR_INVALID_ARG, "tokens too large");
+  if (tokens > most) return fail(UW_ERR_INVALID_ARG, "tokens too large");
   return UW_OK;
 }
 
@@ -260,7 +261,8 @@ uw_status uw_lora_create(int64_t rows, int64_t cols, int32_t slots, int32_t max_
   h->max_rank = max_rank;
   h->rank16 = (max_rank + 15) / 16 * 16;
   h->device = dev;
-  const size_t each = size_t(slots) * h->rank16 * 2, na = align256(each * cols), nb = align256(each * rows);
+  h->rows64 = (rows + 63) / 64 * 64;
+  const size_t each = size_t(slots) * h->rank16 * 2, na = align256(each * cols), nb = align256(each * h->rows64);
   const size_t nt = align256(size_t(slots) * sizeof(uw::LoraSlot));
   if (hipMalloc(&h->mem, na + nb + nt) != hipSuccess) {
     delete h;
@@ -291,7 +293,7 @@ uw_status uw_lora_load(uw_lora h, int32_t slot, const uint16_t* a_dev, const uin
   if (dev != h->device) return fail(UW_ERR_INVALID_ARG, "the adapters are on device %d, current is %d", h->device, dev);
   const int64_t r16 = h->rank16;
   UW_HIP(uw::launch_lora_load(a_dev, b_dev, h->rows, h->cols, rank, scale, h->a + slot * r16 * h->cols,
-                              h->b + slot * r16 * h->rows, h->table + slot, static_cast<hipStream_t>(stream)));
+                              h->b + slot * r16 * h->rows64, h->table + slot, static_cast<hipStream_t>(stream)));
   return UW_OK;
 }
 
@@ -303,14 +305,14 @@ void uw_lora_free(uw_lora h) {
 }
 
 size_t uw_lora_plan_bytes(int64_t tokens, int32_t slots) {
-  if (tokens < 1 || tokens > kMaxTokens || slots < 1 || slots > uw::kGroupMax) return 0;
+  if (tokens < 1 || tokens > kMaxLoraTokens || slots < 1 || slots > uw::kGroupMax) return 0;
   return plan_parts(tokens, slots).total;
 }
 
 uw_status uw_lora_plan(const int32_t* slot_dev, int64_t tokens, int32_t slots, void* plan_dev, size_t plan_bytes,
                        void* stream) {
   if (!slot_dev) return fail(UW_ERR_INVALID_ARG, "null argument");
-  uw_status st = check_tokens(tokens);
+  uw_status st = check_tokens(tokens, kMaxLoraTokens);
   if (st != UW_OK || (st = check_slots(slots)) != UW_OK) return st;
   if ((st = check_plan(plan_dev, plan_bytes, tokens, slots)) != UW_OK) return st;
   if (!aligned(slot_dev, 4)) return fail(UW_ERR_INVALID_ARG, "misaligned pointer");
@@ -332,7 +334,7 @@ uw_status uw_lora_plan(const int32_t* slot_dev, int64_t tokens, int32_t slots, v
 }
 
 size_t uw_lora_workspace_bytes(const uw_lora* adapters, int32_t n, int64_t tokens) {
-  if (!adapters || n < 1 || n > uw::kLoraMaxProj || tokens < 1 || tokens > kMaxTokens) return 0;
+  if (!adapters || n < 1 || n > uw::kLoraMaxProj || tokens < 1 || tokens > kMaxLoraTokens) return 0;
   size_t total = 0;
   for (int i = 0; i < n; ++i) {
     if (!adapters[i]) return 0;
@@ -349,7 +351,7 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
   if (!adapters || !x_dev || !ys_dev || !ldy || !work_dev || (bases_dev && !ldbase))
     return fail(UW_ERR_INVALID_ARG, "null argument");
   if (n < 1 || n > uw::kLoraMaxProj) return fail(UW_ERR_INVALID_ARG, "n must be 1..%d projections", uw::kLoraMaxProj);
-  uw_status st = check_tokens(tokens);
+  uw_status st = check_tokens(tokens, kMaxLoraTokens);
   if (st != UW_OK) return st;
   for (int i = 0; i < n; ++i) {
     if (!adapters[i] || !ys_dev[i]) return fail(UW_ERR_INVALID_ARG, "null adapters or output %d", i);

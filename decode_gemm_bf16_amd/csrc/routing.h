@@ -62,9 +62,13 @@ struct LoraSlot {
   int32_t rank;
   float scale;
 };
-// One projection's adapters: slot i's A is a + i * rank16 * cols, [rank16,
-// cols] bf16, and its B is b + i * rank16 * rows, [rank16 / 16][rows][16] bf16;
-// ranks past the slot's own are zero up to the next multiple of 16.
+// One projection's adapters, both matrices in the order of the matrix
+// operands.  Slot i's A is a + i * rank16 * cols, [rank16 / 16][cols / 32][4][16][8]
+// bf16 with rank r of a block of 16 and column 8 q + i of a step of 32 at
+// [q][r][i].  Its B is b + i * rank16 * rows64 (rows rounded up to 64),
+// [rank16 / 16][rows64 / 64][4][16][4][4] bf16 with row 4 r + j of a group of 64
+// and rank 4 q + i of a block of 16 at [q][r][j][i].  Ranks past the slot's own
+// are zero up to the next multiple of 16.
 struct LoraProj {
   const uint16_t* a;
   const uint16_t* b;

@@ -426,14 +426,14 @@ uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, con
  * layer, y[t] = base[t] + scale_i * B_i (A_i x[t]) for the token's slot i, on
  * top of uw_matmul's output.  Products accumulate in float32 and A_i x[t] is
  * never rounded below it.  The calls run on `stream` and except create and
- * free only launch kernels, so they can be captured. */
+ * free only launch kernels, so they can be captured.  1 <= tokens <= 2^20. */
 typedef struct uw_adapters* uw_lora;
 #define UW_LORA_MAX_RANK 256
 
 /* rows a multiple of 16, cols of 64 (at most 2^23 each), 1..4000 slots of up to
  * max_rank ranks (1..UW_LORA_MAX_RANK).  All slots start empty (rank 0: no
- * adapter).  Device memory: slots * max_rank (rounded up to 16) * (rows +
- * cols) * 2 bytes. */
+ * adapter).  Device memory: slots * max_rank (rounded up to 16) * (rows, rounded
+ * up to 64, + cols) * 2 bytes. */
 uw_status uw_lora_create(int64_t rows, int64_t cols, int32_t slots, int32_t max_rank, uw_lora* out);
 /* Copy an adapter into a slot, replacing what it held: a_dev [rank, cols] and
  * b_dev [rows, rank], contiguous bf16; 0 <= rank <= max_rank (0 empties the
