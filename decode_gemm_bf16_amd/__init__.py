@@ -9,6 +9,7 @@ package loads the library and fails loudly if it has not been built
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -388,41 +389,82 @@ def grouped_matmul(experts, x, y, row_offsets, pipeline: int = P_AUTO) -> None:
 # ---- routing of tokens to experts and back, low-rank adapters ----
 #
 # These calls check what the C side cannot see of a tensor: its type, shape,
-# strides and device.
+# strides and device.  A decode step calls them hundreds of times, on kernels
+# of a few microseconds, so a check costs one attribute of the tensor each.
+
+_torch = None
 
 
-def _tensor(t, name: str, dtypes: str, *shape, rows_strided: bool = False):
-    """``t`` as a tensor of one of the types named, on the current device, of this
-    shape (None: any size) and contiguous (or, rows_strided, with contiguous rows)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _device() -> int:
+    """The current GPU's index (-2 without one: no tensor's device has that index)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    try:
+        return _torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _reject(t, name: str, dtypes, shape, rows: bool = False) -> None:
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if str(t.dtype)[6:] not in dtypes.split("|"):
-        raise TypeError(f"{name} must be {dtypes}, not {t.dtype}")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not (t.is_contiguous() or (rows_strided and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1])):
-        raise ValueError(f"{name} must be contiguous" + (" along its rows" if rows_strided else ""))
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current GPU, not {t.device}")
+    if not (t.is_contiguous() or (rows and t.stride(1) == 1 and (t.stride(0) >= t.shape[1] or t.shape[0] == 1))):
+        raise ValueError(f"{name} must be contiguous" + (" along its rows, which do not overlap" if rows else ""))
+    raise ValueError(f"{name} must be on the current GPU, not {t.device}")
+
+
+def _tensor(t, name: str, dtypes, shape, dev: int) -> int:
+    """Address of ``t``: contiguous, of one of the types, this shape and device."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _reject(t, name, dtypes, shape)
     return t.data_ptr()
 
 
-def _stride(t) -> int:
-    """Row stride in elements (a single row's stride does not matter)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, name: str, dtypes, shape, dev: int) -> tuple[int, int]:
+    """Address and row stride (elements) of a 2-D ``t`` whose rows are contiguous."""
+    if isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        st = t.stride()
+        if shape[0] == 1 and st[1] == 1:
+            return t.data_ptr(), shape[1]
+        if st[1] == 1 and st[0] >= shape[1]:
+            return t.data_ptr(), st[0]
+    _reject(t, name, dtypes, shape, True)
 
 
-def _bytes(t, name: str) -> tuple[int, int]:
+def _shape2(t, name: str):
+    """The shape of a 2-D tensor."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    s = t.shape
+    if len(s) != 2:
+        raise ValueError(f"{name} must have two dimensions, not {len(s)}")
+    return s
+
+
+def _bytes(t, name: str, dev: int) -> tuple[int, int]:
     """Address and size of a workspace tensor of any type and shape (None: 0, 0)."""
     if t is None:
         return 0, 0
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device() or not t.is_contiguous():
+    if not isinstance(t, _torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and on the current GPU")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
+def _types():
+    f, h, i = _torch.float32, _torch.bfloat16, _torch.int32
+    return (f,), (h,), (i,), (f, h)
+
+
+@functools.lru_cache(maxsize=64)
 def _route_config(experts, top_k, score, groups, top_groups, group_score, renormalise, scale) -> RouteConfig:
     return RouteConfig(experts, top_k, score, groups, top_groups, group_score, int(bool(renormalise)), scale)
 
@@ -431,14 +473,17 @@ def route(logits, experts, weights, score: int = SCORE_SOFTMAX, bias=None, group
           group_score: int = GROUP_MAX, renormalise: bool = True, scale: float = 1.0, stream=None) -> None:
     """Choose each token's experts (``uw_route``): logits [tokens, E] float32 or
     bfloat16 -> experts [tokens, top_k] int32 and weights [tokens, top_k] float32."""
-    lp = _tensor(logits, "logits", "float32|bfloat16", None, None, rows_strided=True)
-    t, e = logits.shape
-    ep = _tensor(experts, "experts", "int32", t, None)
-    k = experts.shape[1]
+    dev = _device()
+    f32, _, i32, either = _types()
+    shape = t, e = _shape2(logits, "logits")
+    lp, ld = _rows(logits, "logits", either, shape, dev)
+    out = _shape2(experts, "experts")
+    k = out[1]
     cfg = _route_config(e, k, score, groups, top_groups, group_score, renormalise, scale)
-    _check(_lib.uw_route(lp, F32 if logits.element_size() == 4 else BF16, _stride(logits), t,
-                         0 if bias is None else _tensor(bias, "bias", "float32", e), C.byref(cfg), ep,
-                         _tensor(weights, "weights", "float32", t, k), _stream_ptr(stream)))
+    _check(_lib.uw_route(lp, F32 if logits.dtype == f32[0] else BF16, ld, t,
+                         None if bias is None else _tensor(bias, "bias", f32, (e,), dev), cfg,
+                         _tensor(experts, "experts", i32, (t, k), dev), _tensor(weights, "weights", f32, out, dev),
+                         _stream_ptr(stream)))
 
 
 def group_rows_workspace_bytes(n: int, groups: int) -> int:
@@ -448,35 +493,43 @@ def group_rows_workspace_bytes(n: int, groups: int) -> int:
 def group_rows(index, groups: int, offsets, order, slot, work=None, stream=None) -> None:
     """Stable counting sort of index (int32, any shape, n entries) into groups
     (``uw_group_rows``): offsets [groups + 1], order [n] and slot (index's shape), int32."""
-    ip = _tensor(index, "index", "int32", *index.shape)
+    dev = _device()
+    i32 = _types()[2]
+    shape = index.shape
+    ip = _tensor(index, "index", i32, shape, dev)
     n = index.numel()
-    wp, wb = _bytes(work, "work")
-    _check(_lib.uw_group_rows(ip, n, groups, _tensor(offsets, "offsets", "int32", groups + 1),
-                              _tensor(order, "order", "int32", n), _tensor(slot, "slot", "int32", *index.shape), wp, wb,
+    wp, wb = _bytes(work, "work", dev)
+    _check(_lib.uw_group_rows(ip, n, groups, _tensor(offsets, "offsets", i32, (groups + 1,), dev),
+                              _tensor(order, "order", i32, (n,), dev), _tensor(slot, "slot", i32, shape, dev), wp, wb,
                               _stream_ptr(stream)))
 
 
 def dispatch_rows(x, slot, xs, stream=None) -> None:
     """xs[slot[t, j]] = x[t] (``uw_dispatch_rows``): x [tokens, cols] bfloat16, slot
     [tokens, top_k] int32, xs [rows, cols] bfloat16."""
-    xp = _tensor(x, "x", "bfloat16", None, None, rows_strided=True)
-    t, c = x.shape
-    sp = _tensor(slot, "slot", "int32", t, None)
-    op = _tensor(xs, "xs", "bfloat16", None, c)
-    _check(_lib.uw_dispatch_rows(xp, _stride(x), sp, t, slot.shape[1], c, op, xs.shape[0], _stream_ptr(stream)))
+    dev = _device()
+    _, bf16, i32, _ = _types()
+    shape = t, c = _shape2(x, "x")
+    xp, ld = _rows(x, "x", bf16, shape, dev)
+    k = _shape2(slot, "slot")[1]
+    rows = _shape2(xs, "xs")[0]
+    _check(_lib.uw_dispatch_rows(xp, ld, _tensor(slot, "slot", i32, (t, k), dev), t, k, c,
+                                 _tensor(xs, "xs", bf16, (rows, c), dev), rows, _stream_ptr(stream)))
 
 
 def combine_rows(ys, slot, weights, y, base=None, stream=None) -> None:
     """y[t] = base[t] + sum_j weights[t, j] * ys[slot[t, j]] (``uw_combine_rows``): ys
     [rows, cols] float32, y [tokens, cols] float32 or bfloat16, base float32 or None."""
-    yp = _tensor(ys, "ys", "float32", None, None)
-    rows, c = ys.shape
-    sp = _tensor(slot, "slot", "int32", None, None)
-    t, k = slot.shape
-    op = _tensor(y, "y", "float32|bfloat16", t, c)
-    _check(_lib.uw_combine_rows(yp, rows, sp, _tensor(weights, "weights", "float32", t, k), t, k, c,
-                                0 if base is None else _tensor(base, "base", "float32", t, c), op,
-                                F32 if y.element_size() == 4 else BF16, _stream_ptr(stream)))
+    dev = _device()
+    f32, _, i32, either = _types()
+    shape = rows, c = _shape2(ys, "ys")
+    yp = _tensor(ys, "ys", f32, shape, dev)
+    entries = t, k = _shape2(slot, "slot")
+    _check(_lib.uw_combine_rows(yp, rows, _tensor(slot, "slot", i32, entries, dev),
+                                _tensor(weights, "weights", f32, entries, dev), t, k, c,
+                                None if base is None else _tensor(base, "base", f32, (t, c), dev),
+                                _tensor(y, "y", either, (t, c), dev), F32 if y.dtype == f32[0] else BF16,
+                                _stream_ptr(stream)))
 
 
 def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
@@ -491,16 +544,18 @@ def moe_forward(mats, pipelines, logits, x, y, work, top_k: int, score: int = SC
     n = len(mats)
     if n == 0 or n % 3:
         raise ValueError("mats must hold gate, up and down of each expert")
-    lp = _tensor(logits, "logits", "float32|bfloat16", None, n // 3, rows_strided=True)
-    t, hidden = logits.shape[0], mats[0].cols
+    dev = _device()
+    f32, bf16, _, either = _types()
+    t, hidden = _shape2(logits, "logits")[0], mats[0].cols
+    lp, ld = _rows(logits, "logits", either, (t, n // 3), dev)
     cfg = _route_config(n // 3, top_k, score, groups, top_groups, group_score, renormalise, scale)
-    wp, wb = _bytes(work, "work")
+    wp, wb = _bytes(work, "work", dev)
     _check(_lib.uw_moe_forward((C.c_void_p * n)(*[m.handle for m in mats]), (C.c_int32 * 3)(*pipelines), lp,
-                               F32 if logits.element_size() == 4 else BF16, _stride(logits),
-                               0 if bias is None else _tensor(bias, "bias", "float32", n // 3), C.byref(cfg),
-                               _tensor(x, "x", "bfloat16", t, hidden),
-                               0 if base is None else _tensor(base, "base", "float32", t, hidden),
-                               _tensor(y, "y", "float32", t, hidden), t, wp, wb))
+                               F32 if logits.dtype == f32[0] else BF16, ld,
+                               None if bias is None else _tensor(bias, "bias", f32, (n // 3,), dev), cfg,
+                               _tensor(x, "x", bf16, (t, hidden), dev),
+                               None if base is None else _tensor(base, "base", f32, (t, hidden), dev),
+                               _tensor(y, "y", f32, (t, hidden), dev), t, wp, wb))
 
 
 class Adapters:
@@ -518,9 +573,11 @@ class Adapters:
 
     def load(self, slot: int, a, b, scale: float = 1.0, stream=None) -> None:
         """Copy A [rank, cols] and B [rows, rank] (bfloat16, on the GPU) into a slot (``uw_lora_load``)."""
-        ap = _tensor(a, "a", "bfloat16", None, self.cols)
-        bp = _tensor(b, "b", "bfloat16", self.rows, a.shape[0])
-        _check(_lib.uw_lora_load(self._h, slot, ap, bp, a.shape[0], scale, _stream_ptr(stream)))
+        dev = _device()
+        bf16 = _types()[1]
+        rank = _shape2(a, "a")[0]
+        _check(_lib.uw_lora_load(self._h, slot, _tensor(a, "a", bf16, (rank, self.cols), dev),
+                                 _tensor(b, "b", bf16, (self.rows, rank), dev), rank, scale, _stream_ptr(stream)))
 
     def clear(self, slot: int, stream=None) -> None:
         """Empty a slot: its tokens have no adapter."""
@@ -538,15 +595,21 @@ class Adapters:
             pass
 
 
+_VP = [C.c_void_p * n for n in range(5)]
+_I64 = [C.c_int64 * n for n in range(5)]
+
+
 def lora_plan_bytes(tokens: int, slots: int) -> int:
     return _lib.uw_lora_plan_bytes(tokens, slots)
 
 
 def lora_plan(index, slots: int, plan, stream=None) -> None:
     """Sort a batch's tokens by adapter slot (``uw_lora_plan``): index [tokens] int32."""
-    ip = _tensor(index, "index", "int32", None)
-    pp, pb = _bytes(plan, "plan")
-    _check(_lib.uw_lora_plan(ip, index.shape[0], slots, pp, pb, _stream_ptr(stream)))
+    dev = _device()
+    n = index.numel()
+    ip = _tensor(index, "index", _types()[2], (n,), dev)
+    pp, pb = _bytes(plan, "plan", dev)
+    _check(_lib.uw_lora_plan(ip, n, slots, pp, pb, _stream_ptr(stream)))
 
 
 def lora_workspace_bytes(adapters, tokens: int) -> int:
@@ -556,21 +619,27 @@ def lora_workspace_bytes(adapters, tokens: int) -> int:
 
 def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
     """ys[i] = bases[i] + scale * B (A x) per token for each projection's ``Adapters``
-    (``uw_lora_apply``); bases None: in place, on top of what ys hold.  A base
-    may be None by itself (zeros)."""
+    (``uw_lora_apply``, 1 to 4 of them); bases None: in place, on top of what ys
+    hold.  A base may be None by itself (zeros)."""
     n = len(adapters)
     if bases is None:
         bases = ys
-    if len(ys) != n or len(bases) != n:
-        raise ValueError("adapters, ys and bases must have one length")
-    xp = _tensor(x, "x", "bfloat16", None, adapters[0].cols if n else None, rows_strided=True)
-    t = x.shape[0]
-    yp = [_tensor(y, "ys", "float32", t, a.rows, rows_strided=True) for a, y in zip(adapters, ys)]
-    bp = [None if b is None else _tensor(b, "bases", "float32", t, a.rows, rows_strided=True)
-          for a, b in zip(adapters, bases)]
-    pp, pb = _bytes(plan, "plan")
-    wp, wb = _bytes(work, "work")
-    _check(_lib.uw_lora_apply((C.c_void_p * n)(*[a.handle for a in adapters]), n, pp, pb, xp, _stride(x),
-                              (C.c_void_p * n)(*bp), (C.c_int64 * n)(*[0 if b is None else _stride(b) for b in bases]),
-                              (C.c_void_p * n)(*yp), (C.c_int64 * n)(*[_stride(y) for y in ys]), t, wp, wb,
-                              _stream_ptr(stream)))
+    if not 1 <= n <= 4 or len(ys) != n or len(bases) != n:
+        raise ValueError("adapters, ys and bases must have one length, 1 to 4")
+    dev = _device()
+    f32, bf16, _, _ = _types()
+    t = _shape2(x, "x")[0]
+    xp, ldx = _rows(x, "x", bf16, (t, adapters[0].cols), dev)
+    hs, yp, ldy, bp, ldb = _VP[n](), _VP[n](), _I64[n](), _VP[n](), _I64[n]()
+    for i, a in enumerate(adapters):
+        hs[i] = a._h.value
+        shape = (t, a.rows)
+        y, b = ys[i], bases[i]
+        yp[i], ldy[i] = _rows(y, "ys", f32, shape, dev)
+        if b is y:
+            bp[i], ldb[i] = yp[i], ldy[i]
+        elif b is not None:
+            bp[i], ldb[i] = _rows(b, "bases", f32, shape, dev)
+    pp, pb = _bytes(plan, "plan", dev)
+    wp, wb = _bytes(work, "work", dev)
+    _check(_lib.uw_lora_apply(hs, n, pp, pb, xp, ldx, bp, ldb, yp, ldy, t, wp, wb, _stream_ptr(stream)))
