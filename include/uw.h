@@ -358,7 +358,7 @@ typedef struct {
  * chosen if renormalise (a sum of 0 leaves zeros), times scale.
  * An expert is no candidate where its logit is -inf or NaN, or its c is -inf
  * or NaN (a bias of -inf switches it off for all tokens); its score is 0.  A
- * logit of +inf counts as the largest finite value.  Choices that a token has
+ * logit of +inf counts as its type's largest finite value.  Choices that a token has
  * no candidates left for get expert -1 and weight 0.
  * logits_dev: [tokens, experts] of `type` (UW_F32 or UW_BF16), row stride ld
  * elements (ld >= experts); bias_dev: float [experts] or NULL; experts_dev

@@ -20,11 +20,11 @@ SOFTMAX, SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
 
 
-def _clean(logits: np.ndarray) -> np.ndarray:
-    """NaN counts as -inf (no candidate), +inf as the largest finite float32."""
+def _clean(logits: np.ndarray, largest: float) -> np.ndarray:
+    """NaN counts as -inf (no candidate), +inf as the type's largest finite value."""
     v = np.asarray(logits, dtype=np.float64).copy()
     v[np.isnan(v)] = -np.inf
-    return np.minimum(v, float(np.finfo(np.float32).max))
+    return np.minimum(v, largest)
 
 
 def _scores(l: np.ndarray, score: int) -> np.ndarray:
@@ -47,9 +47,9 @@ def _order(values) -> list[int]:
 
 
 def route(logits, top_k, score=SOFTMAX, bias=None, groups=1, top_groups=1, group_score=GROUP_MAX, renormalise=True,
-          scale=1.0):
+          scale=1.0, largest=float(np.finfo(np.float32).max)):
     """(experts [tokens, top_k] int32, weights [tokens, top_k] float64)."""
-    logits = _clean(logits)
+    logits = _clean(logits, largest)
     tokens, n = logits.shape
     experts = np.full((tokens, top_k), -1, dtype=np.int32)
     weights = np.zeros((tokens, top_k))

@@ -28,6 +28,39 @@ def bf16(torch, v):
     return torch.from_numpy(np.asarray(v, dtype=np.float32)).to(torch.bfloat16)
 
 
+def within_64_bits(l, chosen, bias, kw):
+    """A choice other than the oracle's, which has to be right up to the roundings of
+    64-bit values, and its weights.  Both sides take a score from an exponential
+    and a division (each within 1 ulp, 2^-52), the softmax's sum (the same factor on
+    all scores of a token), a sum with the bias and one of two scores: merits or
+    choices that the two sides order differently are at most 2 x 4 x 2^-52 of the
+    largest apart.  Logits that decide have no rounding."""
+    groups, top_groups = kw.get("groups", 1), kw.get("top_groups", 1)
+    pairs = kw.get("group_score", 0)
+    s = routing._scores(l, kw.get("score", 0))
+    valued = s if bias is None else s + bias.astype(np.float64)
+    assert np.isfinite(l).all() and np.isfinite(valued).all(), "only finite values can be this close"
+    choice, tol = (l, 0.0) if bias is None else (valued, 2.0 ** -49 * np.abs(valued).max())
+    per = len(l) // groups
+    allowed = np.ones(len(l), dtype=bool)
+    if groups > 1:
+        merit = [sorted((valued if pairs else choice)[g * per:(g + 1) * per])[-1 - pairs:] for g in range(groups)]
+        merit = np.array([sum(m) for m in merit])
+        slack = 2.0 ** -49 * np.abs(merit).max() if pairs or bias is not None else 0.0
+        kept = sorted(set(chosen // per) | set(np.argsort(-merit, kind="stable")[:top_groups]),
+                      key=lambda g: (g not in chosen // per, -merit[g]))[:top_groups]
+        dropped = [g for g in range(groups) if g not in kept]
+        assert min(merit[kept]) >= max(merit[dropped]) - slack
+        allowed = np.isin(np.arange(len(l)) // per, kept)
+    assert len(set(chosen)) == len(chosen) and allowed[chosen].all()
+    c = choice[chosen]
+    assert (c[1:] <= c[:-1] + tol).all()
+    rest = np.setdiff1d(np.nonzero(allowed)[0], chosen)
+    assert not len(rest) or choice[rest].max() <= c[-1] + tol
+    w = s[chosen]
+    return (w / w.sum() if kw.get("renormalise", True) else w) * kw.get("scale", 1.0)
+
+
 def run_route(env, logits, top_k, dtype="float32", pad=0, bias=None, **kw):
     """Routes numpy logits and compares with the oracle on the values the GPU saw."""
     torch, uw = env
@@ -41,9 +74,11 @@ def run_route(env, logits, top_k, dtype="float32", pad=0, bias=None, **kw):
     print(f"route {t}x{e} k={top_k} {dtype} pad={pad} {kw}", flush=True)
     uw.route(wide[:, :e], experts, weights, bias=b, **kw)
     torch.cuda.synchronize()
-    want_e, want_w = routing.route(seen, top_k, bias=None if bias is None else b.cpu().numpy(), **kw)
-    assert np.array_equal(experts.cpu().numpy(), want_e)
-    got = weights.cpu().numpy().astype(np.float64)
+    want_e, want_w = routing.route(seen, top_k, bias=None if bias is None else b.cpu().numpy(),
+                                   largest=torch.finfo(wide.dtype).max, **kw)
+    got_e, got = experts.cpu().numpy(), weights.cpu().numpy().astype(np.float64)
+    for row in np.nonzero((got_e != want_e).any(axis=1))[0]:
+        want_w[row] = within_64_bits(seen[row].astype(np.float64), got_e[row], None if b is None else b.cpu().numpy(), kw)
     # below the smallest normal float32 a rounding is absolute
     assert (np.abs(got - want_w) <= WEIGHT_TOL * np.abs(want_w) + 2.0 ** -149).all()
     return want_e, want_w
@@ -120,6 +155,44 @@ def test_route_close_scores(env):
     for groups, pairs in ((1, 0), (4, 0), (4, 1)):
         run_route(env, l, 4, score=1, bias=np.full(16, 0.25), groups=groups, top_groups=min(2, groups), group_score=pairs)
         run_route(env, l, 4, score=1, groups=groups, top_groups=min(2, groups), group_score=pairs)
+
+
+@pytest.mark.parametrize("tokens", [40, 2000])
+@pytest.mark.parametrize("experts,top_k", [(64, 8), (256, 15), (256, 16)])
+@pytest.mark.parametrize("score", [0, 1])
+def test_route_near_ties(env, tokens, experts, top_k, score):
+    """Choices that differ by less than a float32 rounding, by more and not at all,
+    next to each other and in runs: logits in clusters of neighbouring floats, and
+    biases that bring far logits' scores within a few 2^-24 of each other."""
+    rng = np.random.default_rng(experts + top_k)
+    l = rng.normal(size=(tokens, 6))[:, rng.integers(0, 6, size=experts)].astype(np.float32)
+    l = l + rng.integers(-2, 3, size=l.shape).astype(np.float32) * np.spacing(np.abs(l))
+    few = rng.random(tokens) < 0.5  # half of the tokens: spread out, with single close pairs
+    l[few] = rng.normal(size=(int(few.sum()), experts)).astype(np.float32) * 2
+    l[few, 3] = np.nextafter(l[few, 9], np.float32(9))
+    l[0] = 0.0
+    l[0, ::2] = -0.0
+    level = np.full(experts, 0.75) + rng.integers(-3, 4, size=experts) * 2.0 ** -24
+    for groups, top_groups, pairs in ((1, 1, 0), (8, 3, 1), (8, 3, 0), (4, 4, 1)):
+        if top_k <= experts // groups * top_groups:
+            for bias in (None, np.zeros(experts), level):
+                run_route(env, l, top_k, score=score, bias=bias, groups=groups, top_groups=top_groups, group_score=pairs)
+    # all scores + bias nearly equal: bias = 1 - score, rounded
+    flat = rng.normal(size=experts).astype(np.float32)
+    s = 1 / (1 + np.exp(-flat.astype(np.float64)))
+    run_route(env, np.tile(flat, (tokens, 1)), top_k, score=1, bias=(1 - s))
+
+
+def test_route_largest_values(env):
+    """+inf is the type's largest finite value, equal to that value itself."""
+    for dtype, largest in (("bfloat16", 3.3895313892515355e38), ("float32", float(np.finfo(np.float32).max))):
+        l = np.full((3, 8), 1.0)
+        l[0, 5], l[0, 2] = INF, largest
+        l[1, 2], l[1, 5] = INF, largest
+        l[2, 7] = -largest
+        for score in (0, 1):
+            for bias in (None, np.zeros(8)):
+                run_route(env, l, 3, dtype=dtype, score=score, bias=bias, renormalise=False)
 
 
 def test_route_strides_and_alignment(env):
