@@ -13,8 +13,6 @@ namespace uw {
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxGroups = 64;
 constexpr int kRouteMaxTopK = 64;
-// From this many tokens on a token takes 16 lanes instead of 64.
-constexpr int64_t kRouteManyTokens = 1024;
 struct RouteArgs {
   const void* logits;  // [tokens, ld] float32 or bf16
   const float* bias;   // [experts] or null

@@ -29,7 +29,14 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {  // round to nearest even
 constexpr int64_t kOneBlock = 8192;
 constexpr int kMaxBlocks = 256;
 
-int waves_of(int32_t groups) { return groups < 1000 ? 16 : groups < 2000 ? 8 : 4; }  // counters within 64 KB
+// Waves of a workgroup: their counters and the labels' totals stay within 64 KB of LDS.
+int waves_of(int32_t groups) { return groups < 900 ? 16 : groups < 1700 ? 8 : groups < 3000 ? 4 : 2; }
+
+// Waves of the single workgroup: one for each 64 entries, up to waves_of.
+int waves_one(int64_t n, int32_t groups) {
+  const int64_t want = (n + 63) / 64, most = waves_of(groups);
+  return (int)(want < most ? want : most);
+}
 
 // Entries per workgroup: a multiple of 64 per wave, at most kMaxBlocks of them.
 int64_t chunk_of(int64_t n, int waves) {
@@ -78,52 +85,54 @@ __device__ __forceinline__ int block_scan(int v, int* wsum) {
 
 template <bool MULTI>
 __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t chunk) {
-  extern __shared__ int ctr[];  // [waves][groups + 1]
+  extern __shared__ int ctr[];  // [waves][groups + 1], then each label's total, later its first position
   __shared__ int wsum[16];
   const int labels = a.groups + 1, nw = blockDim.x >> 6, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int* const base = ctr + nw * labels;
   for (int i = threadIdx.x; i < nw * labels; i += blockDim.x) ctr[i] = 0;
   __syncthreads();
   const int64_t sec = chunk / nw;
   const int64_t lo = blockIdx.x * chunk + w * sec, hi = lo + sec < a.n ? lo + sec : a.n;
   count_section(a, ctr + w * labels, lo, hi, lane);
   __syncthreads();
-  // this thread's labels, their counts over all entries and in the workgroups before
+  // this thread's labels: their counts over all entries and in the workgroups before
   const int per = (labels + blockDim.x - 1) / blockDim.x;
   const int g0 = threadIdx.x * per, g1 = g0 + per < labels ? g0 + per : labels;
-  auto all_of = [&](int g) {
-    int c = 0;
-    if (MULTI) {
-      for (int b = 0; b < (int)gridDim.x; ++b) c += a.work[(int64_t)b * labels + g];
-    } else {
-      for (int i = 0; i < nw; ++i) c += ctr[i * labels + g];
-    }
-    return c;
-  };
   int sum = 0, tiles = 0;
   for (int g = g0; g < g1; ++g) {
-    const int c = all_of(g);
-    sum += c;
-    tiles += (c + kPlanTile - 1) / kPlanTile;
-  }
-  int base = block_scan(sum, wsum);
-  const bool plan = a.header && blockIdx.x == 0;
-  int tile = plan ? block_scan(tiles, wsum) : 0;
-  for (int g = g0; g < g1; ++g) {
-    const int c = all_of(g);
-    if (blockIdx.x == 0 && a.offsets) a.offsets[g] = base;
-    if (plan)
-      for (int r = 0; r < c; r += kPlanTile)
-        a.tiles[tile++] = PlanTile{base + r, c - r < kPlanTile ? c - r : kPlanTile, g < a.groups ? g : -1, 0};
-    int run = base;
-    if (MULTI)
-      for (int b = 0; b < (int)blockIdx.x; ++b) run += a.work[(int64_t)b * labels + g];
+    int all = 0, run = 0;
+    if (MULTI) {
+      const int32_t* h = a.work + g;
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int v = h[(int64_t)b * labels];
+        all += v;
+        run += b < (int)blockIdx.x ? v : 0;
+      }
+    }
     for (int i = 0; i < nw; ++i) {
       const int v = ctr[i * labels + g];
       ctr[i * labels + g] = run;
       run += v;
     }
-    base += c;
-    if (plan && g == labels - 1) *a.header = PlanHeader{(int32_t)a.n, a.groups, tile, 0};
+    if (!MULTI) all = run;
+    base[g] = all;
+    sum += all;
+    tiles += (all + kPlanTile - 1) / kPlanTile;
+  }
+  int first = block_scan(sum, wsum);
+  const bool plan = a.header && blockIdx.x == 0;
+  int tile = plan ? block_scan(tiles, wsum) : 0;
+  for (int g = g0; g < g1; ++g) {
+    const int c = base[g];
+    base[g] = first;
+    if (blockIdx.x == 0 && a.offsets) a.offsets[g] = first;
+    if (plan) {
+      for (int r = 0; r < c; r += kPlanTile)
+        a.tiles[tile++] = PlanTile{first + r, c - r < kPlanTile ? c - r : kPlanTile, g < a.groups ? g : -1, 0};
+      if (g == labels - 1) *a.header = PlanHeader{(int32_t)a.n, a.groups, tile, 0};
+    }
+    first += c;
   }
   __syncthreads();
   int bits = 0;
@@ -140,7 +149,7 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
     if (there) {
-      const int at = mine[g] + rank;
+      const int at = base[g] + mine[g] + rank;
       a.order[at] = (int32_t)i;
       if (a.slot) a.slot[i] = g < a.groups ? at : -1;
     }
@@ -208,10 +217,11 @@ size_t group_work_bytes(int64_t n, int32_t groups) {
 }
 
 hipError_t launch_group_rows(const GroupArgs& a, hipStream_t s) {
-  const int waves = waves_of(a.groups), labels = a.groups + 1;
+  const bool one = a.n <= kOneBlock;
+  const int waves = one ? waves_one(a.n, a.groups) : waves_of(a.groups), labels = a.groups + 1;
   const int64_t chunk = chunk_of(a.n, waves);
-  const size_t lds = size_t(waves) * labels * 4;
-  if (a.n <= kOneBlock) {
+  const size_t lds = size_t(waves + 1) * labels * 4;
+  if (one) {
     hipLaunchKernelGGL(group_place_kernel<false>, dim3(1), dim3(64 * waves), lds, s, a, chunk);
     return hipGetLastError();
   }
