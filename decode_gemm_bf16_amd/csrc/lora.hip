@@ -181,7 +181,7 @@ __device__ __forceinline__ void stage_parts(const LoraArgs& a, const LoraProj& p
 // is token q + 4 k of 16, so that up to 4 KM tokens take the first KM of a lane's
 // 4 results.  B lies in the order of the operands: a lane's 4 x 4 values of a
 // group and rank block are 32 bytes.
-template <int NS, int KM, int C>
+template <int NS, int KM, int C, bool STREAM>
 __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int reps,
                                             LoraParts& parts) {
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -222,7 +222,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
 #pragma unroll
           for (int i = 0; i < NS; ++i)
 #pragma unroll
-            for (int k = 0; k < KM; ++k) v[c][i][k] = *(const f32x4*)(p.base + (int64_t)tok[i][k] * p.ldbase + nc);
+            for (int k = 0; k < KM; ++k) v[c][i][k] = __builtin_nontemporal_load((const f32x4*)(p.base + (int64_t)tok[i][k] * p.ldbase + nc));
         }
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -270,15 +270,21 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
         for (int i = 0; i < NS; ++i)
 #pragma unroll
           for (int k = 0; k < KM; ++k)
-            if (i0 + i * 16 + q + 4 * k < tile.len && n < p.rows)
-              *(f32x4*)(p.y + (int64_t)tok[i][k] * p.ldy + n) =
-                  f32x4{acc[c][i][0][k], acc[c][i][1][k], acc[c][i][2][k], acc[c][i][3][k]};
+            if (i0 + i * 16 + q + 4 * k < tile.len && n < p.rows) {
+              const f32x4 v = {acc[c][i][0][k], acc[c][i][1][k], acc[c][i][2][k], acc[c][i][3][k]};
+              f32x4* to = (f32x4*)(p.y + (int64_t)tok[i][k] * p.ldy + n);
+              if constexpr (STREAM)
+                __builtin_nontemporal_store(v, to);
+              else
+                *to = v;
+            }
       }
     }
 }
 
-// C: groups of 64 rows per wave; two at once where the tile has at most 4 tokens.
-template <int C>
+// C: groups of 64 rows per wave; two at once where the tile has at most 4
+// tokens.  STREAM: y passes the caches by.
+template <int C, bool STREAM>
 __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraArgs a) {
   __shared__ __attribute__((aligned(16))) LoraParts parts;
   const LoraProj& p = a.proj[blockIdx.z];
@@ -287,11 +293,20 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
   const PlanTile tile = a.tiles[blockIdx.y];
   constexpr int kFew = C > 2 ? 2 : C;
   if (tile.len <= 4)
-    expand_tile<1, 1, kFew>(a, p, tile, C / kFew, parts);
+    expand_tile<1, 1, kFew, STREAM>(a, p, tile, C / kFew, parts);
   else if (C > 1 || tile.len <= 32)
-    expand_tile<2, 4, 1>(a, p, tile, C, parts);
+    expand_tile<2, 4, 1, STREAM>(a, p, tile, C, parts);
   else
-    expand_tile<4, 4, 1>(a, p, tile, C, parts);
+    expand_tile<4, 4, 1, STREAM>(a, p, tile, C, parts);
+}
+
+template <int C>
+void launch_expand(const LoraArgs& a, int rows, hipStream_t s) {
+  const dim3 grid((rows + 256 * C - 1) / (256 * C), a.tiles_max, a.nproj);
+  if (a.stream)
+    hipLaunchKernelGGL((lora_expand_kernel<C, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((lora_expand_kernel<C, false>), grid, dim3(256), 0, s, a);
 }
 
 // ---- loading an adapter into a slot ----
@@ -325,7 +340,7 @@ int64_t lora_tiles_max(int64_t tokens, int32_t slots) {
 
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj) {
   const int64_t blocks = (lora_tiles_max(tokens, slots) + tokens / kPlanTile) * nproj, steps = cols / 32;
-  int k = 8;
+  int k = 4;
   while (k > 1 && (k * blocks > 512 || steps < k * kShrinkWaves)) k /= 2;
   return k;
 }
@@ -340,9 +355,9 @@ hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(lora_shrink_kernel, dim3(2 * a.tiles_max * a.ksplit, 1, rblocks * a.nproj), dim3(64 * kShrinkWaves),
                      0, s, a);
   if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
-    hipLaunchKernelGGL(lora_expand_kernel<4>, dim3((rows + 1023) / 1024, a.tiles_max, a.nproj), dim3(256), 0, s, a);
+    launch_expand<4>(a, rows, s);
   else
-    hipLaunchKernelGGL(lora_expand_kernel<1>, dim3((rows + 255) / 256, a.tiles_max, a.nproj), dim3(256), 0, s, a);
+    launch_expand<1>(a, rows, s);
   return hipGetLastError();
 }
 

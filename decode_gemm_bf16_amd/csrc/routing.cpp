@@ -372,6 +372,7 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
   const PlanParts parts = plan_parts(tokens, slots);
   const uint8_t* m = static_cast<const uint8_t*>(plan_dev);
   uw::LoraArgs a{};
+  int64_t written = 0;
   a.ksplit = uw::lora_ksplit(tokens, slots, cols, n);
   uint8_t* cur = static_cast<uint8_t*>(work_dev);
   for (int i = 0; i < n; ++i) {
@@ -403,6 +404,7 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
     p.ldy = ldy[i];
     p.rows = (int32_t)h->rows;
     p.rank16 = h->rank16;
+    written += tokens * h->rows * 4;
     p.part = reinterpret_cast<float*>(cur);
     cur += align256(size_t(a.ksplit) * size_t(tokens) * h->rank16 * 4);
   }
@@ -419,6 +421,7 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
   a.slots = slots;
   a.cols = (int32_t)cols;
   a.nproj = n;
+  a.stream = written >= (int64_t(128) << 20);  // half of the 256 MB Infinity Cache
   a.tiles_max = (int32_t)uw::lora_tiles_max(tokens, slots);
   UW_HIP(uw::launch_lora_apply(a, static_cast<hipStream_t>(stream)));
   return UW_OK;

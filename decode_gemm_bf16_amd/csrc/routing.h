@@ -87,6 +87,7 @@ struct LoraArgs {
   const uint16_t* x;
   int64_t ldx;
   int32_t tokens, slots, cols, nproj, ksplit, tiles_max;
+  bool stream;  // y passes the caches by
 };
 // Workgroups along K of the product with A (a rule on sizes alone).
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj);

@@ -26,7 +26,7 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {  // round to nearest even
 // kernel writes each workgroup's counts and in the second each workgroup sums
 // the counts of those before it by itself.
 
-constexpr int64_t kOneBlock = 8192;
+constexpr int64_t kOneBlock = 4096;
 constexpr int kMaxBlocks = 256;
 
 // Waves of a workgroup: their counters and the labels' totals stay within 64 KB of LDS.
@@ -52,8 +52,18 @@ __device__ __forceinline__ int label_of(const GroupArgs& a, int64_t i) {
   return (uint32_t)v < (uint32_t)a.groups ? v : a.groups;
 }
 
-__device__ __forceinline__ void count_section(const GroupArgs& a, int* ctr, int64_t lo, int64_t hi, int lane) {
-  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&ctr[label_of(a, i)], 1);
+// Counts entries lo + t, lo + t + step, ... < hi of this thread.  Entries of one
+// label stand together in many batches (a request's tokens): a wave whose 64 are
+// equal adds them at once instead of one after the other.
+__device__ __forceinline__ void count(const GroupArgs& a, int* ctr, int64_t lo, int64_t hi, int t, int step) {
+  for (int64_t i = lo + t; i < hi; i += step) {
+    const int g = label_of(a, i), first = __builtin_amdgcn_readfirstlane(g);
+    const uint64_t there = __ballot(true);
+    if (__ballot(g == first) != there)
+      atomicAdd(&ctr[g], 1);
+    else if ((threadIdx.x & 63) == __builtin_ctzll(there))
+      atomicAdd(&ctr[g], (int)__popcll(there));
+  }
 }
 
 __global__ __launch_bounds__(1024) void group_count_kernel(GroupArgs a, int64_t chunk) {
@@ -62,7 +72,7 @@ __global__ __launch_bounds__(1024) void group_count_kernel(GroupArgs a, int64_t 
   for (int g = threadIdx.x; g < labels; g += blockDim.x) ctr[g] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < a.n ? lo + chunk : a.n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) atomicAdd(&ctr[label_of(a, i)], 1);
+  count(a, ctr, lo, hi, threadIdx.x, blockDim.x);
   __syncthreads();
   for (int g = threadIdx.x; g < labels; g += blockDim.x) a.work[(int64_t)blockIdx.x * labels + g] = ctr[g];
 }
@@ -93,7 +103,7 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
   __syncthreads();
   const int64_t sec = chunk / nw;
   const int64_t lo = blockIdx.x * chunk + w * sec, hi = lo + sec < a.n ? lo + sec : a.n;
-  count_section(a, ctr + w * labels, lo, hi, lane);
+  count(a, ctr + w * labels, lo, hi, lane, 64);
   __syncthreads();
   // this thread's labels: their counts over all entries and in the workgroups before
   const int per = (labels + blockDim.x - 1) / blockDim.x;
