@@ -25,59 +25,79 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRankBlock = 64;        // ranks per shrink workgroup and per staging of v
 constexpr int kShrinkWaves = 8;
+constexpr int kLoraMaxSplit = 8;
 
 __device__ __forceinline__ bool plan_has(const LoraArgs& a, int tile) {
   return a.header->tokens == a.tokens && a.header->slots == a.slots && tile < a.header->tiles;
 }
 
+union ShrinkLds {
+  u32x4 turn[kShrinkWaves][512];  // a wave's 64 tokens x 64 columns
+  float red[kShrinkWaves][16][kRankBlock];
+};
+
 // ---- shrink ----
 //
-// One workgroup: half a tile (32 tokens from i0 on), up to 64 ranks, one of
-// ksplit parts of cols, which its 8 waves divide among them in 32-column steps.
-// A lies in the order of the operands (1 KB for 16 ranks x 32 columns);
-// a wave holds all NS x NR blocks of 16 tokens x 16 ranks, so that a step's
-// NS + NR loads of 16 bytes a lane feed NS * NR matrix instructions, and U steps'
-// loads are in flight at once.  The waves' sums are added in LDS.
-template <int NS, int NR, int U>
-__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int i0,
-                                            int kpart, int rblock, int nr, float (&red)[kShrinkWaves][16][kRankBlock]) {
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int steps = a.cols / 32, parts = a.ksplit * kShrinkWaves, part = kpart * kShrinkWaves + w;
-  const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-  const uint16_t* ar[NR];
-  const uint16_t* xr[NS];
+// One workgroup: one tile, or 32 tokens of it (`halves`) where there are tiles
+// enough to fill the CUs so, up to 64 ranks, one of ksplit parts of cols, whose
+// batches of 64 columns its 8 waves take in turn (together 1 KB of each row at a
+// time).  A wave holds all NS x NR blocks of 16 tokens x 16 ranks.  A lies in the
+// order of the operands (1 KB for 16 ranks x 32 columns).  x goes from memory to
+// the wave's part of LDS 128 bytes of a row at a time and is read from there in
+// that order: loads of 64 bytes of 16 rows, as the operands have it, waste most
+// of a memory page's activation.  The waves' sums are added in LDS.
+// Bound by what a CU takes in at memory latency, about 22 GB/s each, so the work
+// is spread over all of them before anything else.
+template <int NS, int NR>
+__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int kpart,
+                                            int rblock, int nr, ShrinkLds& lds) {
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int batches = a.cols / 64, per = (batches + a.ksplit - 1) / a.ksplit;
+  const int b0 = kpart * per, b1 = b0 + per < batches ? b0 + per : batches;
+  // a slot's A is less than 2^32 bytes: one address for the wave, 32-bit offsets
+  const uint16_t* const abase = p.a + ((int64_t)tile.slot * p.rank16 + rblock * kRankBlock) * a.cols;
+  // Load i: tokens 8 i + lane / 8, 16 bytes of each 128 a lane.  A lane takes the
+  // piece (lane ^ token) % 8, so that the pieces that a read of the operands takes
+  // at once lie in different banks.
+  int tok[2 * NS];
 #pragma unroll
-  for (int j = 0; j < NR; ++j)  // blocks past the adapter's ranks repeat the first; they are not stored
-    ar[j] = p.a + ((int64_t)tile.slot * p.rank16 + rblock * kRankBlock + (j < nr ? j : 0) * 16) * a.cols + lane * 8;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int k = i0 + i * 16 + r;  // rows past the tile's end repeat its last
-    xr[i] = a.x + (int64_t)a.order[tile.start + (k < tile.len ? k : tile.len - 1)] * a.ldx + q * 8;
+  for (int i = 0; i < 2 * NS; ++i) {
+    const int k = 8 * i + (lane >> 3);  // rows past the tile's end repeat its last
+    tok[i] = a.order[tile.start + (k < tile.len ? k : tile.len - 1)];
   }
+  const int piece = ((lane ^ (lane >> 3)) & 7) * 8;
+  u32x4* const turn = lds.turn[w];
   f32x4 acc[NS][NR] = {};
-  for (int s = s0; s < s1; s += U) {
-    bf16x8 xv[U][NS], av[U][NR];
+  for (int b = b0 + w; b < b1; b += kShrinkWaves) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {  // steps past the last repeat the batch's first
-      const int64_t at = s + u < s1 ? s + u : s;
+    for (int i = 0; i < 2 * NS; ++i)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(a.x + ((int64_t)tok[i] * a.ldx + b * 64 + piece)),
+          (__attribute__((address_space(3))) void*)(turn + i * 64), 16, 0, 0);
+    bf16x8 av[2][NR];
 #pragma unroll
-      for (int j = 0; j < NR; ++j) av[u][j] = *(const bf16x8*)(ar[j] + at * 512);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) xv[u][i] = *(const bf16x8*)(xr[i] + at * 32);
-    }
-    __builtin_amdgcn_sched_barrier(0);  // all loads in flight before the first product
+      for (int j = 0; j < NR; ++j)  // blocks past the adapter's ranks repeat the first; they are not stored
+        av[u][j] = *(const bf16x8*)(abase + (uint32_t)((j < nr ? j : 0) * 16 * a.cols + (b * 2 + u) * 512 + lane * 8));
+    __builtin_amdgcn_s_waitcnt(0);  // all of it in flight, then all of it there
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s + u >= s1) break;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
+      for (int i = 0; i < NS; ++i) {
+        const u32x4 xf = turn[(i * 16 + r) * 8 + ((4 * u + q) ^ (r & 7))];
 #pragma unroll
         for (int j = 0; j < NR; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[u][i], av[u][j], acc[i][j], 0, 0, 0);
-    }
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf), av[u][j], acc[i][j], 0, 0, 0);
+      }
+    // the reads have left LDS before the next batch's loads write it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
+  __syncthreads();  // the waves' parts of LDS become the sums'
+  float(&red)[kShrinkWaves][16][kRankBlock] = lds.red;
   // block (i, j): token 4 q + k of subtile i, rank 16 j + r
-  float* out = p.part + ((int64_t)kpart * a.tokens + tile.start + i0) * p.rank16 + rblock * kRankBlock;
+  float* out = p.part + ((int64_t)kpart * a.tokens + tile.start) * p.rank16 + rblock * kRankBlock;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     if (i) __syncthreads();
@@ -87,7 +107,7 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p
       for (int k = 0; k < 4; ++k) red[w][4 * q + k][16 * j + r] = acc[i][j][k];
     __syncthreads();
     const int rk = threadIdx.x % (NR * 16);
-    for (int tk = threadIdx.x / (NR * 16); tk < 16 && i0 + i * 16 + tk < tile.len; tk += 64 * kShrinkWaves / (NR * 16)) {
+    for (int tk = threadIdx.x / (NR * 16); tk < 16 && i * 16 + tk < tile.len; tk += 64 * kShrinkWaves / (NR * 16)) {
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < kShrinkWaves; ++k) v += red[k][tk][rk];
@@ -97,31 +117,35 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p
 }
 
 __global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_shrink_kernel(LoraArgs a) {
-  __shared__ float red[kShrinkWaves][16][kRankBlock];
+  __shared__ __attribute__((aligned(16))) ShrinkLds lds;
   const LoraProj& p = a.proj[blockIdx.z % a.nproj];
-  const int rblock = blockIdx.z / a.nproj;
-  const int half = blockIdx.x / a.ksplit, kpart = blockIdx.x - half * a.ksplit, i0 = (half & 1) * 32;
-  if (!plan_has(a, half >> 1)) return;
-  const PlanTile tile = a.tiles[half >> 1];
-  if (tile.slot < 0 || i0 >= tile.len) return;
+  const int rblock = blockIdx.z / a.nproj, kpart = blockIdx.x;
+  const int at = a.halves ? blockIdx.y >> 1 : blockIdx.y, i0 = a.halves ? (blockIdx.y & 1) * 32 : 0;
+  if (!plan_has(a, at)) return;
+  PlanTile tile = a.tiles[at];
+  tile.slot = __builtin_amdgcn_readfirstlane(tile.slot);
+  tile.start = __builtin_amdgcn_readfirstlane(tile.start) + i0;
+  tile.len = __builtin_amdgcn_readfirstlane(tile.len) - i0;
+  if (tile.slot < 0 || tile.len <= 0) return;
+  if (a.halves && tile.len > 32) tile.len = 32;
   const int rank = p.table[tile.slot].rank - rblock * kRankBlock;
   if (rank <= 0) return;
-  const int nr = rank >= kRankBlock ? kRankBlock / 16 : (rank + 15) / 16;
-  if (tile.len - i0 <= 16) {
+  const int nr = __builtin_amdgcn_readfirstlane(rank >= kRankBlock ? kRankBlock / 16 : (rank + 15) / 16);
+  auto run = [&](auto ns) {
+    constexpr int NS = decltype(ns)::value;
     if (nr == 1)
-      shrink_tile<1, 1, 4>(a, p, tile, i0, kpart, rblock, nr, red);
+      shrink_tile<NS, 1>(a, p, tile, kpart, rblock, nr, lds);
     else if (nr == 2)
-      shrink_tile<1, 2, 4>(a, p, tile, i0, kpart, rblock, nr, red);
+      shrink_tile<NS, 2>(a, p, tile, kpart, rblock, nr, lds);
     else
-      shrink_tile<1, 4, 3>(a, p, tile, i0, kpart, rblock, nr, red);
-  } else {
-    if (nr == 1)
-      shrink_tile<2, 1, 4>(a, p, tile, i0, kpart, rblock, nr, red);
-    else if (nr == 2)
-      shrink_tile<2, 2, 3>(a, p, tile, i0, kpart, rblock, nr, red);
-    else
-      shrink_tile<2, 4, 2>(a, p, tile, i0, kpart, rblock, nr, red);
-  }
+      shrink_tile<NS, 4>(a, p, tile, kpart, rblock, nr, lds);
+  };
+  if (tile.len <= 16)
+    run(std::integral_constant<int, 1>());
+  else if (tile.len <= 32)
+    run(std::integral_constant<int, 2>());
+  else
+    run(std::integral_constant<int, 4>());
 }
 
 // ---- expand ----
@@ -338,10 +362,18 @@ int64_t lora_tiles_max(int64_t tokens, int32_t slots) {
   return t < tokens ? t : tokens;
 }
 
+// Whether the shrink takes 32 tokens a workgroup: 136 tiles of 4096 columns 20 +
+// 174 us (shrink and expansion) against 19 + 191 with whole tiles in two parts.
+bool lora_halves(int64_t tokens, int32_t slots, int nproj) { return lora_tiles_max(tokens, slots) * nproj >= 128; }
+
+// Parts of cols: up to two workgroups a CU, and two batches for each wave.  (More
+// parts cost the expansion, which reads all of them for every 256 columns of y:
+// 777 tokens on 4096 x 14336 in 4 parts 18.3 + 15.2 us, in 8 14.3 + 18.1.)
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj) {
-  const int64_t blocks = (lora_tiles_max(tokens, slots) + tokens / kPlanTile) * nproj, steps = cols / 32;
-  int k = 4;
-  while (k > 1 && (k * blocks > 512 || steps < k * kShrinkWaves)) k /= 2;
+  const int64_t tiles = lora_tiles_max(tokens, slots) * nproj, batches = cols / 64;
+  const int64_t blocks = lora_halves(tokens, slots, nproj) ? 2 * tiles : tiles;
+  int k = kLoraMaxSplit;
+  while (k > 1 && (k * blocks > 512 || batches < 2 * k * kShrinkWaves)) k /= 2;
   return k;
 }
 
@@ -352,8 +384,8 @@ hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
     rows = a.proj[i].rows > rows ? a.proj[i].rows : rows;
   }
   const unsigned rblocks = (rank16 + kRankBlock - 1) / kRankBlock;
-  hipLaunchKernelGGL(lora_shrink_kernel, dim3(2 * a.tiles_max * a.ksplit, 1, rblocks * a.nproj), dim3(64 * kShrinkWaves),
-                     0, s, a);
+  hipLaunchKernelGGL(lora_shrink_kernel, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),
+                     dim3(64 * kShrinkWaves), 0, s, a);
   if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
     launch_expand<4>(a, rows, s);
   else

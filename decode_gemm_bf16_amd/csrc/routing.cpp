@@ -374,6 +374,7 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
   uw::LoraArgs a{};
   int64_t written = 0;
   a.ksplit = uw::lora_ksplit(tokens, slots, cols, n);
+  a.halves = uw::lora_halves(tokens, slots, n);
   uint8_t* cur = static_cast<uint8_t*>(work_dev);
   for (int i = 0; i < n; ++i) {
     const uw_adapters* h = adapters[i];

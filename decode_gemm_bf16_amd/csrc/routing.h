@@ -87,9 +87,11 @@ struct LoraArgs {
   const uint16_t* x;
   int64_t ldx;
   int32_t tokens, slots, cols, nproj, ksplit, tiles_max;
+  bool halves;  // the shrink takes 32 tokens a workgroup
   bool stream;  // y passes the caches by
 };
-// Workgroups along K of the product with A (a rule on sizes alone).
+// Rules on sizes alone.
+bool lora_halves(int64_t tokens, int32_t slots, int nproj);
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj);
 int64_t lora_tiles_max(int64_t tokens, int32_t slots);
 hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s);
