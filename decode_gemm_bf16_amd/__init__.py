@@ -630,16 +630,19 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
     f32, bf16, _, _ = _types()
     t = _shape2(x, "x")[0]
     xp, ldx = _rows(x, "x", bf16, (t, adapters[0].cols), dev)
-    hs, yp, ldy, bp, ldb = _VP[n](), _VP[n](), _I64[n](), _VP[n](), _I64[n]()
-    for i, a in enumerate(adapters):
-        hs[i] = a._h.value
+    hs, yp, ldy, bp, ldb = [], [], [], [], []
+    for a, y, b in zip(adapters, ys, bases):
+        hs.append(a._h.value)
         shape = (t, a.rows)
-        y, b = ys[i], bases[i]
-        yp[i], ldy[i] = _rows(y, "ys", f32, shape, dev)
-        if b is y:
-            bp[i], ldb[i] = yp[i], ldy[i]
-        elif b is not None:
-            bp[i], ldb[i] = _rows(b, "bases", f32, shape, dev)
+        p, ld = _rows(y, "ys", f32, shape, dev)
+        yp.append(p)
+        ldy.append(ld)
+        if b is not y:
+            p, ld = (None, 0) if b is None else _rows(b, "bases", f32, shape, dev)
+        bp.append(p)
+        ldb.append(ld)
+    vp, i64 = _VP[n], _I64[n]
     pp, pb = _bytes(plan, "plan", dev)
     wp, wb = _bytes(work, "work", dev)
-    _check(_lib.uw_lora_apply(hs, n, pp, pb, xp, ldx, bp, ldb, yp, ldy, t, wp, wb, _stream_ptr(stream)))
+    _check(_lib.uw_lora_apply(vp(*hs), n, pp, pb, xp, ldx, vp(*bp), i64(*ldb), vp(*yp), i64(*ldy), t, wp, wb,
+                              _stream_ptr(stream)))

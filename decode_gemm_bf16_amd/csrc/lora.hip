@@ -26,6 +26,13 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kRankBlock = 64;        // ranks per shrink workgroup and per staging of v
 constexpr int kShrinkWaves = 8;
 constexpr int kLoraMaxSplit = 8;
+// A of at most this size a workgroup of lora_one_kernel reads for itself.  One
+// launch against two, gate and up of 14336 x 4096 in a graph: 16 ranks (128 KB)
+// 5.5 against 6.9 us at one token and 7.5 against 7.7 at four, 32 ranks (256 KB) 7.1
+// against 8.1 and 9.4 against 9.4; above, 16 ranks of 14336 columns (448 KB) 9.6
+// against 8.0 and 64 of 4096 (512 KB) 11.9 against 9.6.  (Not captured, the launch
+// saved is 2.3 us of host time more.)
+constexpr int64_t kLoraOneBytes = 256 << 10;
 
 __device__ __forceinline__ bool plan_has(const LoraArgs& a, int tile) {
   return a.header->tokens == a.tokens && a.header->slots == a.slots && tile < a.header->tiles;
@@ -50,9 +57,9 @@ union ShrinkLds {
 // is spread over all of them before anything else.
 template <int NS, int NR>
 __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int kpart,
-                                            int rblock, int nr, ShrinkLds& lds) {
+                                            int ksplit, int rblock, int nr, ShrinkLds& lds, float* out, int64_t ldout) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int batches = a.cols / 64, per = (batches + a.ksplit - 1) / a.ksplit;
+  const int batches = a.cols / 64, per = (batches + ksplit - 1) / ksplit;
   const int b0 = kpart * per, b1 = b0 + per < batches ? b0 + per : batches;
   // a slot's A is less than 2^32 bytes: one address for the wave, 32-bit offsets
   const uint16_t* const abase = p.a + ((int64_t)tile.slot * p.rank16 + rblock * kRankBlock) * a.cols;
@@ -97,7 +104,6 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p
   __syncthreads();  // the waves' parts of LDS become the sums'
   float(&red)[kShrinkWaves][16][kRankBlock] = lds.red;
   // block (i, j): token 4 q + k of subtile i, rank 16 j + r
-  float* out = p.part + ((int64_t)kpart * a.tokens + tile.start) * p.rank16 + rblock * kRankBlock;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     if (i) __syncthreads();
@@ -111,7 +117,7 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < kShrinkWaves; ++k) v += red[k][tk][rk];
-      if (rk < nr * 16) out[(int64_t)(i * 16 + tk) * p.rank16 + rk] = v;
+      if (rk < nr * 16) out[(i * 16 + tk) * ldout + rk] = v;
     }
   }
 }
@@ -131,14 +137,15 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_shrink_kernel(LoraA
   const int rank = p.table[tile.slot].rank - rblock * kRankBlock;
   if (rank <= 0) return;
   const int nr = __builtin_amdgcn_readfirstlane(rank >= kRankBlock ? kRankBlock / 16 : (rank + 15) / 16);
+  float* out = p.part + ((int64_t)kpart * a.tokens + tile.start) * p.rank16 + rblock * kRankBlock;
   auto run = [&](auto ns) {
     constexpr int NS = decltype(ns)::value;
     if (nr == 1)
-      shrink_tile<NS, 1>(a, p, tile, kpart, rblock, nr, lds);
+      shrink_tile<NS, 1>(a, p, tile, kpart, a.ksplit, rblock, nr, lds, out, p.rank16);
     else if (nr == 2)
-      shrink_tile<NS, 2>(a, p, tile, kpart, rblock, nr, lds);
+      shrink_tile<NS, 2>(a, p, tile, kpart, a.ksplit, rblock, nr, lds, out, p.rank16);
     else
-      shrink_tile<NS, 4>(a, p, tile, kpart, rblock, nr, lds);
+      shrink_tile<NS, 4>(a, p, tile, kpart, a.ksplit, rblock, nr, lds, out, p.rank16);
   };
   if (tile.len <= 16)
     run(std::integral_constant<int, 1>());
@@ -165,18 +172,24 @@ __device__ __forceinline__ uint16_t bf16_part(float& v) {
 // the lanes' 8-byte reads of 16 tokens apart in the banks
 typedef uint16_t LoraParts[3][kPlanTile][kRankBlock + 8];
 
-// Thread t of 256: token t / 4, ranks 4 (t % 4) .. + 3 of each 16-rank block.
-__device__ __forceinline__ void stage_parts(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int rank,
-                                            float scale, int r0, int blocks, LoraParts& parts) {
+// Where the products with A stand: [ksplit][token of the tile][ranks].
+struct LoraSource {
+  const float* v;
+  int64_t ld, next;
+  int ksplit;
+};
+
+// Thread t: token t / 4, ranks 4 (t % 4) .. + 3 of each 16-rank block.
+__device__ __forceinline__ void stage_parts(const LoraSource& from, int len, int rank, float scale, int r0, int blocks,
+                                            LoraParts& parts) {
   const int k = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
-  if (k >= tile.len) return;
-  const float* src = p.part + (int64_t)(tile.start + k) * p.rank16 + r0 + c;
-  const int64_t next = (int64_t)a.tokens * p.rank16;
+  if (k >= len) return;
+  const float* src = from.v + k * from.ld + r0 + c;
   f32x4 v[kRankBlock / 16] = {};
-  for (int s = 0; s < a.ksplit; ++s) {
+  for (int s = 0; s < from.ksplit; ++s) {
 #pragma unroll
     for (int i = 0; i < kRankBlock / 16; ++i)  // blocks past the last repeat it
-      v[i] += *(const f32x4*)(src + s * next + (i < blocks ? i : blocks - 1) * 16);
+      v[i] += *(const f32x4*)(src + s * from.next + (i < blocks ? i : blocks - 1) * 16);
   }
 #pragma unroll
   for (int i = 0; i < kRankBlock / 16; ++i) {
@@ -196,8 +209,8 @@ __device__ __forceinline__ void stage_parts(const LoraArgs& a, const LoraProj& p
   }
 }
 
-// One workgroup: one tile; each of its 4 waves takes C groups of 64 rows of B
-// (every fourth one) at once, `reps` times over, and 16 NS tokens at a time.  v is
+// One workgroup: one tile; each of its WAVES waves takes C groups of 64 rows of B
+// (WAVES apart) at once, `reps` times over, and 16 NS tokens at a time.  v is
 // the A operand (16 tokens x 16 ranks) and B the B operand; row 4 r + j of a
 // group is column r of its j-th 16-column product, so that a lane's results of
 // the four products are 4 neighbouring columns of y, and a load or store of 16
@@ -205,9 +218,9 @@ __device__ __forceinline__ void stage_parts(const LoraArgs& a, const LoraProj& p
 // is token q + 4 k of 16, so that up to 4 KM tokens take the first KM of a lane's
 // 4 results.  B lies in the order of the operands: a lane's 4 x 4 values of a
 // group and rank block are 32 bytes.
-template <int NS, int KM, int C, bool STREAM>
-__device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int reps,
-                                            LoraParts& parts) {
+template <int NS, int KM, int C, bool STREAM, int WAVES>
+__device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile,
+                                            const LoraSource& from, int reps, LoraParts& parts) {
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int groups = (p.rows + 63) / 64;
   const uint16_t* b = p.b + (int64_t)(tile.slot < 0 ? 0 : tile.slot) * p.rank16 * groups * 64 + lane * 16;
@@ -216,7 +229,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
   const int nr = (entry.rank + 15) / 16;
   for (int rep = 0; rep < reps; ++rep)
     for (int i0 = 0; i0 < tile.len; i0 += 16 * NS) {
-      const int g0 = (blockIdx.x * reps + rep) * 4 * C + w;
+      const int g0 = (blockIdx.x * reps + rep) * WAVES * C + w;
       int tok[NS][KM];
 #pragma unroll
       for (int i = 0; i < NS; ++i)
@@ -229,7 +242,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
       auto load_b = [&](int rb) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int g = g0 + 4 * c < groups ? g0 + 4 * c : groups - 1;
+          const int g = g0 + WAVES * c < groups ? g0 + WAVES * c : groups - 1;
           const u32x4* src = (const u32x4*)(b + ((int64_t)rb * groups + g) * 1024);
           bv[c][0] = src[0];
           bv[c][1] = src[1];
@@ -242,7 +255,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
         f32x4 v[C][NS][KM];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int n = (g0 + 4 * c) * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4;
+          const int n = (g0 + WAVES * c) * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4;
 #pragma unroll
           for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -261,7 +274,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
         const int blocks = nr - r0 < kRankBlock / 16 ? nr - r0 : kRankBlock / 16;
         if ((rep == 0 && i0 == 0) || nr > kRankBlock / 16) {  // else the parts of all ranks are there
           if (rep || i0 || r0) __syncthreads();
-          stage_parts(a, p, tile, entry.rank, entry.scale, r0 * 16, blocks, parts);
+          stage_parts(from, tile.len, entry.rank, entry.scale, r0 * 16, blocks, parts);
           __syncthreads();
         }
         for (int rb = 0; rb < blocks; ++rb) {
@@ -289,7 +302,7 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int n = (g0 + 4 * c) * 64 + 4 * r;
+        const int n = (g0 + WAVES * c) * 64 + 4 * r;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -316,12 +329,42 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
   if ((int)blockIdx.x * 256 * C >= p.rows) return;
   const PlanTile tile = a.tiles[blockIdx.y];
   constexpr int kFew = C > 2 ? 2 : C;
+  const LoraSource from{p.part + (int64_t)tile.start * p.rank16, p.rank16, (int64_t)a.tokens * p.rank16, a.ksplit};
   if (tile.len <= 4)
-    expand_tile<1, 1, kFew, STREAM>(a, p, tile, C / kFew, parts);
+    expand_tile<1, 1, kFew, STREAM, 4>(a, p, tile, from, C / kFew, parts);
   else if (C > 1 || tile.len <= 32)
-    expand_tile<2, 4, 1, STREAM>(a, p, tile, C, parts);
+    expand_tile<2, 4, 1, STREAM, 4>(a, p, tile, from, C, parts);
   else
-    expand_tile<4, 4, 1, STREAM>(a, p, tile, C, parts);
+    expand_tile<4, 4, 1, STREAM, 4>(a, p, tile, from, C, parts);
+}
+
+// ---- both in one launch, for at most four tokens ----
+//
+// Each workgroup takes 512 rows of B and makes the products with A for itself:
+// A is read rows / 512 times over, from L2 but for the first, and a launch is
+// saved.
+__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) union {
+    ShrinkLds lds;
+    LoraParts parts;
+  } u;
+  __shared__ __attribute__((aligned(16))) float v[4][kRankBlock];
+  const LoraProj& p = a.proj[blockIdx.z];
+  if (!plan_has(a, blockIdx.y)) return;
+  if ((int)blockIdx.x * 512 >= p.rows) return;
+  PlanTile tile = a.tiles[blockIdx.y];
+  tile.slot = __builtin_amdgcn_readfirstlane(tile.slot);
+  tile.start = __builtin_amdgcn_readfirstlane(tile.start);
+  tile.len = __builtin_amdgcn_readfirstlane(tile.len);
+  const int nr = tile.slot < 0 ? 0 : __builtin_amdgcn_readfirstlane((p.table[tile.slot].rank + 15) / 16);
+  if (nr == 1)
+    shrink_tile<1, 1>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+  else if (nr == 2)
+    shrink_tile<1, 2>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+  else if (nr > 2)
+    shrink_tile<1, 4>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+  __syncthreads();
+  expand_tile<1, 1, 1, false, kShrinkWaves>(a, p, tile, LoraSource{v[0], kRankBlock, 0, 1}, 1, u.parts);
 }
 
 template <int C>
@@ -382,6 +425,11 @@ hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
   for (int i = 0; i < a.nproj; ++i) {
     rank16 = a.proj[i].rank16 > rank16 ? a.proj[i].rank16 : rank16;
     rows = a.proj[i].rows > rows ? a.proj[i].rows : rows;
+  }
+  if (a.tokens <= 4 && rank16 <= kRankBlock && (int64_t)rank16 * a.cols * 2 <= kLoraOneBytes) {
+    hipLaunchKernelGGL(lora_one_kernel, dim3((rows + 511) / 512, a.tiles_max, a.nproj), dim3(64 * kShrinkWaves), 0, s,
+                       a);
+    return hipGetLastError();
   }
   const unsigned rblocks = (rank16 + kRankBlock - 1) / kRankBlock;
   hipLaunchKernelGGL(lora_shrink_kernel, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),

@@ -299,8 +299,11 @@ uw_status uw_lora_load(uw_lora h, int32_t slot, const uint16_t* a_dev, const uin
 
 void uw_lora_free(uw_lora h) {
   if (!h) return;
+  int dev = 0;  // the work that may still read the slots runs on the adapters' device
+  const bool other = hipGetDevice(&dev) == hipSuccess && dev != h->device && hipSetDevice(h->device) == hipSuccess;
   (void)hipDeviceSynchronize();
   (void)hipFree(h->mem);
+  if (other) (void)hipSetDevice(dev);
   delete h;
 }
 
