@@ -592,11 +592,65 @@ def moe_bench(torch, uw, synth, stream, steps, warmup, n_experts=8, top_k=2, tok
                                 "speedup": round(bms / ms, 3)}
         log(f"moe grouped {tokens}: " + json.dumps(grouped[str(tokens)]))
     res["grouped"] = grouped
-    for m in experts:
-        m.free()
     del wds
     torch.cuda.empty_cache()
+    res["layer"] = moe_layer_bench(torch, uw, synth, stream, experts, top_k, steps, warmup, tokens_list)
+    for m in experts:
+        m.free()
+    torch.cuda.empty_cache()
     return res
+
+
+def moe_layer_bench(torch, uw, synth, stream, gates, top_k, steps, warmup, tokens_list) -> dict:
+    """A whole layer of SwiGLU experts (uw_moe_forward, direct palette): gates as
+    given, ups their copies, downs copies of one [hidden, inter] matrix.  layer_us
+    is the wall clock of a call with new logits each time, its wait for the
+    group sizes included; routing_us is the same layer's routing, grouping,
+    dispatch and combination alone, in a graph."""
+    n, rows, cols = len(gates), gates[0].rows, gates[0].cols
+    c = synth.CONFIGS["mlp_8b"]
+    ups = [g.clone() for g in gates]
+    downs = [uw.Matrix(synth.weights(cols, rows, 210, c["p"], c["shift"]), uw.FMT_PALETTE)]
+    downs += [downs[0].clone() for _ in range(n - 1)]
+    mats = [m for three in zip(gates, ups, downs) for m in three]
+    for m in mats:
+        m.set_streams(stream)
+    out = {}
+    for tokens in tokens_list:
+        r = tokens * top_k
+        logits = [torch.randn((tokens, n), device="cuda") for _ in range(8)]
+        x = uw.bf16_tensor(synth.activations(tokens, cols, xseed=tokens))
+        y = torch.empty((tokens, cols), device="cuda")
+        work = torch.empty(uw.moe_workspace_bytes(tokens, cols, rows, n, top_k), dtype=torch.uint8, device="cuda")
+        calls = max(20, steps // 10)
+        for i in range(warmup + calls):
+            if i == warmup:
+                torch.cuda.synchronize()
+                t0 = time.perf_counter()
+            uw.moe_forward(mats, [uw.P4_DIRECT_PALETTE] * 3, logits[i % 8], x, y, work, top_k)
+        torch.cuda.synchronize()
+        layer_us = (time.perf_counter() - t0) / calls * 1e6
+        e = torch.empty((tokens, top_k), dtype=torch.int32, device="cuda")
+        w, slot = torch.empty((tokens, top_k), device="cuda"), torch.empty_like(e)
+        offsets = torch.empty(n + 1, dtype=torch.int32, device="cuda")
+        order = torch.empty(r, dtype=torch.int32, device="cuda")
+        gw = torch.empty(uw.group_rows_workspace_bytes(r, n), dtype=torch.uint8, device="cuda")
+        xs = torch.empty((r, cols), dtype=torch.bfloat16, device="cuda")
+        ys = torch.zeros((r, cols), device="cuda")
+        k = [0]
+
+        def routing():
+            uw.route(logits[k[0] % 8], e, w, stream=stream)
+            uw.group_rows(e, n, offsets, order, slot, gw, stream=stream)
+            uw.dispatch_rows(x, slot, xs, stream=stream)
+            uw.combine_rows(ys, slot, w, y, stream=stream)
+            k[0] += 1
+        ms = time_graph(torch, routing, steps=calls, warmup=warmup, stream=stream)
+        out[str(tokens)] = {"layer_us": round(layer_us, 2), "routing_us": round(ms * 1e3, 2)}
+        log(f"moe layer {tokens}: " + json.dumps(out[str(tokens)]))
+    for m in ups + downs:
+        m.free()
+    return out
 
 
 def bundle_load_bench(uw, w, reps: int = 3) -> dict:

@@ -392,15 +392,17 @@ def grouped_matmul(experts, x, y, row_offsets, pipeline: int = P_AUTO) -> None:
 # strides and device.  A decode step calls them hundreds of times, on kernels
 # of a few microseconds, so a check costs one attribute of the tensor each.
 
-_torch = None
+_torch = _Tensor = _f32 = _bf16 = _i32 = _either = None
 
 
 def _device() -> int:
     """The current GPU's index (-2 without one: no tensor's device has that index)."""
-    global _torch
+    global _torch, _Tensor, _f32, _bf16, _i32, _either
     if _torch is None:
         import torch
-        _torch = torch
+        _Tensor, _torch = torch.Tensor, torch
+        _f32, _bf16, _i32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+        _either = _f32 + _bf16
     try:
         return _torch.cuda.current_device()
     except (RuntimeError, AssertionError):
@@ -408,7 +410,7 @@ def _device() -> int:
 
 
 def _reject(t, name: str, dtypes, shape, rows: bool = False) -> None:
-    if not isinstance(t, _torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, not {t.dtype}")
@@ -421,7 +423,7 @@ def _reject(t, name: str, dtypes, shape, rows: bool = False) -> None:
 
 def _tensor(t, name: str, dtypes, shape, dev: int) -> int:
     """Address of ``t``: contiguous, of one of the types, this shape and device."""
-    if not (isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
             and t.is_contiguous()):
         _reject(t, name, dtypes, shape)
     return t.data_ptr()
@@ -429,7 +431,7 @@ def _tensor(t, name: str, dtypes, shape, dev: int) -> int:
 
 def _rows(t, name: str, dtypes, shape, dev: int) -> tuple[int, int]:
     """Address and row stride (elements) of a 2-D ``t`` whose rows are contiguous."""
-    if isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+    if isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
         if t.is_contiguous():
             return t.data_ptr(), shape[1]
         st = t.stride()
@@ -442,7 +444,7 @@ def _rows(t, name: str, dtypes, shape, dev: int) -> tuple[int, int]:
 
 def _shape2(t, name: str):
     """The shape of a 2-D tensor."""
-    if not isinstance(t, _torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     s = t.shape
     if len(s) != 2:
@@ -454,14 +456,9 @@ def _bytes(t, name: str, dev: int) -> tuple[int, int]:
     """Address and size of a workspace tensor of any type and shape (None: 0, 0)."""
     if t is None:
         return 0, 0
-    if not isinstance(t, _torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and on the current GPU")
     return t.data_ptr(), t.nbytes
-
-
-def _types():
-    f, h, i = _torch.float32, _torch.bfloat16, _torch.int32
-    return (f,), (h,), (i,), (f, h)
 
 
 @functools.lru_cache(maxsize=64)
@@ -474,15 +471,14 @@ def route(logits, experts, weights, score: int = SCORE_SOFTMAX, bias=None, group
     """Choose each token's experts (``uw_route``): logits [tokens, E] float32 or
     bfloat16 -> experts [tokens, top_k] int32 and weights [tokens, top_k] float32."""
     dev = _device()
-    f32, _, i32, either = _types()
     shape = t, e = _shape2(logits, "logits")
-    lp, ld = _rows(logits, "logits", either, shape, dev)
+    lp, ld = _rows(logits, "logits", _either, shape, dev)
     out = _shape2(experts, "experts")
     k = out[1]
     cfg = _route_config(e, k, score, groups, top_groups, group_score, renormalise, scale)
-    _check(_lib.uw_route(lp, F32 if logits.dtype == f32[0] else BF16, ld, t,
-                         None if bias is None else _tensor(bias, "bias", f32, (e,), dev), cfg,
-                         _tensor(experts, "experts", i32, (t, k), dev), _tensor(weights, "weights", f32, out, dev),
+    _check(_lib.uw_route(lp, F32 if logits.dtype == _f32[0] else BF16, ld, t,
+                         None if bias is None else _tensor(bias, "bias", _f32, (e,), dev), cfg,
+                         _tensor(experts, "experts", _i32, (t, k), dev), _tensor(weights, "weights", _f32, out, dev),
                          _stream_ptr(stream)))
 
 
@@ -494,13 +490,12 @@ def group_rows(index, groups: int, offsets, order, slot, work=None, stream=None)
     """Stable counting sort of index (int32, any shape, n entries) into groups
     (``uw_group_rows``): offsets [groups + 1], order [n] and slot (index's shape), int32."""
     dev = _device()
-    i32 = _types()[2]
     shape = index.shape
-    ip = _tensor(index, "index", i32, shape, dev)
+    ip = _tensor(index, "index", _i32, shape, dev)
     n = index.numel()
     wp, wb = _bytes(work, "work", dev)
-    _check(_lib.uw_group_rows(ip, n, groups, _tensor(offsets, "offsets", i32, (groups + 1,), dev),
-                              _tensor(order, "order", i32, (n,), dev), _tensor(slot, "slot", i32, shape, dev), wp, wb,
+    _check(_lib.uw_group_rows(ip, n, groups, _tensor(offsets, "offsets", _i32, (groups + 1,), dev),
+                              _tensor(order, "order", _i32, (n,), dev), _tensor(slot, "slot", _i32, shape, dev), wp, wb,
                               _stream_ptr(stream)))
 
 
@@ -508,27 +503,25 @@ def dispatch_rows(x, slot, xs, stream=None) -> None:
     """xs[slot[t, j]] = x[t] (``uw_dispatch_rows``): x [tokens, cols] bfloat16, slot
     [tokens, top_k] int32, xs [rows, cols] bfloat16."""
     dev = _device()
-    _, bf16, i32, _ = _types()
     shape = t, c = _shape2(x, "x")
-    xp, ld = _rows(x, "x", bf16, shape, dev)
+    xp, ld = _rows(x, "x", _bf16, shape, dev)
     k = _shape2(slot, "slot")[1]
     rows = _shape2(xs, "xs")[0]
-    _check(_lib.uw_dispatch_rows(xp, ld, _tensor(slot, "slot", i32, (t, k), dev), t, k, c,
-                                 _tensor(xs, "xs", bf16, (rows, c), dev), rows, _stream_ptr(stream)))
+    _check(_lib.uw_dispatch_rows(xp, ld, _tensor(slot, "slot", _i32, (t, k), dev), t, k, c,
+                                 _tensor(xs, "xs", _bf16, (rows, c), dev), rows, _stream_ptr(stream)))
 
 
 def combine_rows(ys, slot, weights, y, base=None, stream=None) -> None:
     """y[t] = base[t] + sum_j weights[t, j] * ys[slot[t, j]] (``uw_combine_rows``): ys
     [rows, cols] float32, y [tokens, cols] float32 or bfloat16, base float32 or None."""
     dev = _device()
-    f32, _, i32, either = _types()
     shape = rows, c = _shape2(ys, "ys")
-    yp = _tensor(ys, "ys", f32, shape, dev)
+    yp = _tensor(ys, "ys", _f32, shape, dev)
     entries = t, k = _shape2(slot, "slot")
-    _check(_lib.uw_combine_rows(yp, rows, _tensor(slot, "slot", i32, entries, dev),
-                                _tensor(weights, "weights", f32, entries, dev), t, k, c,
-                                None if base is None else _tensor(base, "base", f32, (t, c), dev),
-                                _tensor(y, "y", either, (t, c), dev), F32 if y.dtype == f32[0] else BF16,
+    _check(_lib.uw_combine_rows(yp, rows, _tensor(slot, "slot", _i32, entries, dev),
+                                _tensor(weights, "weights", _f32, entries, dev), t, k, c,
+                                None if base is None else _tensor(base, "base", _f32, (t, c), dev),
+                                _tensor(y, "y", _either, (t, c), dev), F32 if y.dtype == _f32[0] else BF16,
                                 _stream_ptr(stream)))
 
 
@@ -545,17 +538,16 @@ def moe_forward(mats, pipelines, logits, x, y, work, top_k: int, score: int = SC
     if n == 0 or n % 3:
         raise ValueError("mats must hold gate, up and down of each expert")
     dev = _device()
-    f32, bf16, _, either = _types()
     t, hidden = _shape2(logits, "logits")[0], mats[0].cols
-    lp, ld = _rows(logits, "logits", either, (t, n // 3), dev)
+    lp, ld = _rows(logits, "logits", _either, (t, n // 3), dev)
     cfg = _route_config(n // 3, top_k, score, groups, top_groups, group_score, renormalise, scale)
     wp, wb = _bytes(work, "work", dev)
     _check(_lib.uw_moe_forward((C.c_void_p * n)(*[m.handle for m in mats]), (C.c_int32 * 3)(*pipelines), lp,
-                               F32 if logits.dtype == f32[0] else BF16, ld,
-                               None if bias is None else _tensor(bias, "bias", f32, (n // 3,), dev), cfg,
-                               _tensor(x, "x", bf16, (t, hidden), dev),
-                               None if base is None else _tensor(base, "base", f32, (t, hidden), dev),
-                               _tensor(y, "y", f32, (t, hidden), dev), t, wp, wb))
+                               F32 if logits.dtype == _f32[0] else BF16, ld,
+                               None if bias is None else _tensor(bias, "bias", _f32, (n // 3,), dev), cfg,
+                               _tensor(x, "x", _bf16, (t, hidden), dev),
+                               None if base is None else _tensor(base, "base", _f32, (t, hidden), dev),
+                               _tensor(y, "y", _f32, (t, hidden), dev), t, wp, wb))
 
 
 class Adapters:
@@ -574,10 +566,9 @@ class Adapters:
     def load(self, slot: int, a, b, scale: float = 1.0, stream=None) -> None:
         """Copy A [rank, cols] and B [rows, rank] (bfloat16, on the GPU) into a slot (``uw_lora_load``)."""
         dev = _device()
-        bf16 = _types()[1]
         rank = _shape2(a, "a")[0]
-        _check(_lib.uw_lora_load(self._h, slot, _tensor(a, "a", bf16, (rank, self.cols), dev),
-                                 _tensor(b, "b", bf16, (self.rows, rank), dev), rank, scale, _stream_ptr(stream)))
+        _check(_lib.uw_lora_load(self._h, slot, _tensor(a, "a", _bf16, (rank, self.cols), dev),
+                                 _tensor(b, "b", _bf16, (self.rows, rank), dev), rank, scale, _stream_ptr(stream)))
 
     def clear(self, slot: int, stream=None) -> None:
         """Empty a slot: its tokens have no adapter."""
@@ -607,7 +598,7 @@ def lora_plan(index, slots: int, plan, stream=None) -> None:
     """Sort a batch's tokens by adapter slot (``uw_lora_plan``): index [tokens] int32."""
     dev = _device()
     n = index.numel()
-    ip = _tensor(index, "index", _types()[2], (n,), dev)
+    ip = _tensor(index, "index", _i32, (n,), dev)
     pp, pb = _bytes(plan, "plan", dev)
     _check(_lib.uw_lora_plan(ip, n, slots, pp, pb, _stream_ptr(stream)))
 
@@ -627,18 +618,17 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
     if not 1 <= n <= 4 or len(ys) != n or len(bases) != n:
         raise ValueError("adapters, ys and bases must have one length, 1 to 4")
     dev = _device()
-    f32, bf16, _, _ = _types()
     t = _shape2(x, "x")[0]
-    xp, ldx = _rows(x, "x", bf16, (t, adapters[0].cols), dev)
+    xp, ldx = _rows(x, "x", _bf16, (t, adapters[0].cols), dev)
     hs, yp, ldy, bp, ldb = [], [], [], [], []
     for a, y, b in zip(adapters, ys, bases):
         hs.append(a._h.value)
         shape = (t, a.rows)
-        p, ld = _rows(y, "ys", f32, shape, dev)
+        p, ld = _rows(y, "ys", _f32, shape, dev)
         yp.append(p)
         ldy.append(ld)
         if b is not y:
-            p, ld = (None, 0) if b is None else _rows(b, "bases", f32, shape, dev)
+            p, ld = (None, 0) if b is None else _rows(b, "bases", _f32, shape, dev)
         bp.append(p)
         ldb.append(ld)
     vp, i64 = _VP[n], _I64[n]
