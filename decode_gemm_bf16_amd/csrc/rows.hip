@@ -22,8 +22,10 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {  // round to nearest even
 // position is its counter plus its rank among the equal labels of the 64.  No
 // position depends on the order in which atomics are served.
 //
-// Up to kOneBlock entries one workgroup does all of it.  Beyond, a first
-// kernel writes each workgroup's counts and in the second each workgroup sums
+// Up to kOneBlock entries one workgroup does all of it (in a graph, 8 and 256
+// groups: 1024 entries 4.0 and 4.9 us against 6.1 and 7.1 in two launches, 4096 6.3
+// and 8.6 against 7.3 and 8.9, 8192 9.2 and 13.2 against 7.6 and 9.4).  Beyond, a
+// first kernel writes each workgroup's counts and in the second each workgroup sums
 // the counts of those before it by itself.
 
 constexpr int64_t kOneBlock = 4096;
