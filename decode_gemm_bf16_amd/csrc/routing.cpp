@@ -138,8 +138,10 @@ uw_status route_check(const void* logits, int32_t type, int64_t ld, int64_t toke
   if (!aligned(logits, size) || (bias && !aligned(bias, 4)) || !aligned(experts, 4) || !aligned(weights, 4))
     return fail(UW_ERR_INVALID_ARG, "misaligned pointer");
   const size_t in = span(tokens, c->experts, ld, size), out = size_t(tokens) * c->top_k * 4;
-  if (overlap(logits, in, experts, out) || overlap(logits, in, weights, out) || overlap(experts, out, weights, out))
-    return fail(UW_ERR_INVALID_ARG, "outputs overlap the logits or each other");
+  const size_t nb = bias ? size_t(c->experts) * 4 : 0;
+  if (overlap(logits, in, experts, out) || overlap(logits, in, weights, out) || overlap(experts, out, weights, out) ||
+      (bias && (overlap(bias, nb, experts, out) || overlap(bias, nb, weights, out))))
+    return fail(UW_ERR_INVALID_ARG, "outputs overlap an input or each other");
   return UW_OK;
 }
 

@@ -1426,6 +1426,11 @@ uw_status moe_impl(const uw_handle* handles, const int32_t* pipelines, const voi
   const size_t xb = size_t(tokens) * hidden * 2, yb = size_t(tokens) * hidden * 4;
   if (xa % 16 || ya % 16 || ba % 16) return fail(UW_ERR_INVALID_ARG, "x, base and y must be 16-byte aligned");
   auto meet = [](uintptr_t a, size_t na, uintptr_t b, size_t nb) { return a < b + nb && b < a + na; };
+  const uintptr_t la = reinterpret_cast<uintptr_t>(logits), bi = reinterpret_cast<uintptr_t>(bias);
+  const size_t lb = size_t((tokens - 1) * ld + ne) * (type == UW_F32 ? 4 : 2);
+  if (meet(la, lb, wa, need) || meet(la, lb, ya, yb) ||
+      (bias && (meet(bi, size_t(ne) * 4, wa, need) || meet(bi, size_t(ne) * 4, ya, yb))))
+    return fail(UW_ERR_INVALID_ARG, "the logits or the bias overlap y or the workspace");
   if (meet(xa, xb, ya, yb) || meet(wa, need, ya, yb) || meet(wa, need, xa, xb) ||
       (base && (meet(wa, need, ba, yb) || (base != y && meet(ba, yb, ya, yb)))))
     return fail(UW_ERR_INVALID_ARG, "x, base, y and the workspace overlap (base may be y itself)");

@@ -124,6 +124,119 @@ def test_long_batch(env):
     check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
 
 
+def test_wide_outputs_with_few_tokens_a_slot(env):
+    """The form of the expansion for batches of few tokens per slot (1024 columns a
+    workgroup), on tiles of 1, 4, 5, 6 and 64 tokens, with an end inside a workgroup
+    and inside a wave's 64 columns."""
+    rng = np.random.default_rng(20)
+    tokens, slots, rows, cols = 130, 40, 12336, 64
+    s = Setup(env, rng, slots, rows, cols, 20, rng.integers(0, 21, size=slots))
+    index = np.concatenate([np.full(70, 3), np.full(5, 4), np.full(4, 5), np.full(4, -1), rng.integers(6, slots, size=47)])
+    rng.shuffle(index)
+    x, xv = values(rng, tokens, cols)
+    base = rng.standard_normal((tokens, rows), dtype=np.float32)
+    check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
+
+
+def test_output_larger_than_the_caches(env):
+    """y of 128 MiB and more is stored past the caches."""
+    rng = np.random.default_rng(21)
+    tokens, slots, rows, cols = 2100, 3, 16384, 64
+    s = Setup(env, rng, slots, rows, cols, 4, [4, 2, 0])
+    index = np.sort(rng.integers(-1, slots, size=tokens))
+    x, xv = values(rng, tokens, cols)
+    base = rng.standard_normal((tokens, rows), dtype=np.float32)
+    check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
+
+
+@pytest.mark.parametrize("tokens,rows,cols,max_rank,slots", [
+    (40, 64, 4160, 40, 3),    # 65 batches of columns in uneven parts
+    (3, 1040, 8192, 32, 2),   # few tokens, A too large for one launch
+    (4, 1040, 8192, 16, 2),   # A of exactly the size that one launch takes
+    (4, 1040, 8256, 16, 2),   # and past it
+    (100, 64, 14336, 64, 50),
+    (70, 2064, 1024, 256, 1),
+])
+def test_long_columns(env, tokens, rows, cols, max_rank, slots):
+    rng = np.random.default_rng(tokens + cols)
+    s = Setup(env, rng, slots, rows, cols, max_rank, [max(1, max_rank - i % 5) for i in range(slots)])
+    x, xv = values(rng, tokens, cols)
+    index = rng.integers(-1, slots, size=tokens)
+    base = rng.standard_normal((tokens, rows), dtype=np.float32)
+    check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
+
+
+def test_small_magnitudes(env):
+    """Products with A near 2^-110, whose lower parts bf16 holds as denormals."""
+    rng = np.random.default_rng(22)
+    tokens, rows, cols = 20, 64, 64
+    torch, uw = env
+    h = uw.Adapters(1, rows, cols, 16)
+    a = synth.f32_to_bf16_bits(rng.standard_normal((16, cols), dtype=np.float32) * np.float32(2.0 ** -57))
+    b = synth.f32_to_bf16_bits(rng.standard_normal((rows, 16), dtype=np.float32) * np.float32(2.0 ** 60))
+    x = synth.f32_to_bf16_bits(rng.standard_normal((tokens, cols), dtype=np.float32) * np.float32(2.0 ** -57))
+    h.load(0, uw.bf16_tensor(a), uw.bf16_tensor(b), 1.0)
+    s = Setup.__new__(Setup)
+    s.h = h
+    av, bv, xv = (synth.bf16_bits_to_f32(v).astype(np.float64) for v in (a, b, x))
+    base = np.zeros((tokens, rows), dtype=np.float32)
+    index = np.zeros(tokens, dtype=int)
+    check(apply(env, [s], x, index, [base])[0], xv, index, {0: (av, bv, 1.0)}, base)
+
+
+def test_far_offsets(env):
+    """x, base and y whose rows lie past 2^31 elements."""
+    torch, uw = env
+    rng = np.random.default_rng(23)
+    tokens, rows, cols, wide = 40000, 32, 64, 65536
+    s = Setup(env, rng, 2, rows, cols, 4, [4, 3])
+    far = np.sort(rng.choice(np.arange(33000, tokens), size=60, replace=False))
+    index = np.full(tokens, -1)
+    index[far] = rng.integers(0, 2, size=60)
+    index[5] = 1
+    at = np.concatenate([[5], far])
+    xb, xv = values(rng, len(at), cols)
+    base = rng.standard_normal((len(at), rows), dtype=np.float32)
+    x = torch.zeros((tokens, wide), dtype=torch.bfloat16, device="cuda")[:, wide - cols:]
+    y = torch.zeros((tokens, wide), device="cuda")[:, wide - rows:]
+    where = torch.from_numpy(at).cuda()
+    x[where] = uw.bf16_tensor(xb)
+    y[where] = torch.from_numpy(base).cuda()
+    plan = torch.empty(uw.lora_plan_bytes(tokens, 2), dtype=torch.uint8, device="cuda")
+    work = torch.empty(uw.lora_workspace_bytes([s.h], tokens), dtype=torch.uint8, device="cuda")
+    print("lora far offsets", flush=True)
+    uw.lora_plan(torch.from_numpy(index.astype(np.int32)).cuda(), 2, plan)
+    uw.lora_apply([s.h], plan, x, [y], work)
+    torch.cuda.synchronize()
+    check(y[where].cpu().numpy().astype(np.float64), xv, index[at], s.values, base)
+    rest = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    rest[where] = False
+    assert not y[rest].any()
+
+
+def test_two_streams_share_a_plan(env):
+    torch, uw = env
+    rng = np.random.default_rng(24)
+    tokens, slots, cols = 300, 6, 512
+    setups = [Setup(env, rng, slots, rows, cols, 16, rng.integers(0, 17, size=slots)) for rows in (512, 1024)]
+    x, xv = values(rng, tokens, cols)
+    index = rng.integers(-1, slots, size=tokens)
+    bases = [rng.standard_normal((tokens, s.h.rows), dtype=np.float32) for s in setups]
+    xd, bd = uw.bf16_tensor(x), [torch.from_numpy(b).cuda() for b in bases]
+    ys = [torch.empty_like(b) for b in bd]
+    plan = torch.empty(uw.lora_plan_bytes(tokens, slots), dtype=torch.uint8, device="cuda")
+    works = [torch.empty(uw.lora_workspace_bytes([s.h], tokens), dtype=torch.uint8, device="cuda") for s in setups]
+    uw.lora_plan(torch.from_numpy(index.astype(np.int32)).cuda(), slots, plan)
+    streams = [torch.cuda.Stream() for _ in setups]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, st, y, b, w in zip(setups, streams, ys, bd, works):
+            uw.lora_apply([s.h], plan, xd, [y], w, bases=[b], stream=st)
+    torch.cuda.synchronize()
+    for s, y, b in zip(setups, ys, bases):
+        check(y.cpu().numpy().astype(np.float64), xv, index, s.values, b)
+
+
 def test_in_place_strides_and_repeats(env):
     """In place, with x, base and y cut out of wider rows; columns beside stay as
     they were, and the same call gives the same bits."""

@@ -238,11 +238,10 @@ def run_group(env, index, groups):
     return offsets, order, slot
 
 
-@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 1000, 1024, 8191, 8192, 8193, 40000, 131071, 1100003])
-@pytest.mark.parametrize("groups", [1, 2, 8, 60, 255, 256, 999, 1000, 1999, 2000, 4000])
+@pytest.mark.parametrize("n,groups", [(n, g) for n in (1, 2, 63, 64, 65, 1000, 1024, 4095, 4096, 4097, 8193, 40000, 131071)
+                                      for g in (1, 2, 8, 60, 255, 256, 899, 900, 1699, 1700, 2999, 3000, 4000)]
+                         + [(1100003, g) for g in (1, 60, 1000, 2000, 4000)])
 def test_group_sizes(env, n, groups):
-    if n > 131071 and groups not in (1, 60, 4000):
-        pytest.skip("large counts once per kernel shape")
     rng = np.random.default_rng(n + groups)
     index = rng.integers(-1, groups + 1, size=n)  # -1 and groups are ungrouped
     run_group(env, index, groups)
@@ -293,11 +292,9 @@ def test_dispatch(env, tokens, top_k, cols, pad):
 
 @pytest.mark.parametrize("tokens,top_k,cols", [(1, 1, 8), (1, 8, 1032), (65, 3, 520), (130, 8, 4096), (9, 5, 14336),
                                                 (700, 2, 24), (4, 64, 64), (33, 1, 2048)])
-@pytest.mark.parametrize("with_base", ["none", "apart", "in place"])
-@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+@pytest.mark.parametrize("with_base,out", [("none", "float32"), ("apart", "float32"), ("in place", "float32"),
+                                           ("none", "bfloat16"), ("apart", "bfloat16")])
 def test_combine(env, tokens, top_k, cols, with_base, out):
-    if with_base == "in place" and out == "bfloat16":
-        pytest.skip("a bfloat16 output cannot be its float32 base")
     torch, uw = env
     rng = np.random.default_rng(tokens + cols + top_k)
     rows = tokens * top_k + 5
@@ -346,6 +343,58 @@ def test_combine_specials(env):
     y = torch.empty((1, 8), device="cuda", dtype=torch.bfloat16)
     uw.combine_rows(big, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones((1, 1), device="cuda"), y)
     assert torch.equal(y, big.to(torch.bfloat16))
+
+
+def test_dispatch_larger_than_the_caches(env):
+    """Copies of 128 MiB and more are stored past the caches."""
+    torch, uw = env
+    rng = np.random.default_rng(6)
+    tokens, top_k, cols = 4100, 4, 4096
+    slot = rng.permutation(tokens * top_k).reshape(tokens, top_k).astype(np.int32)
+    slot[rng.random(slot.shape) < 0.1] = -1
+    x = torch.randn((tokens, cols), device="cuda").to(torch.bfloat16)
+    xs = torch.full((tokens * top_k, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    s = torch.from_numpy(slot).cuda().long()
+    want = xs.clone()
+    for j in range(top_k):
+        there = s[:, j] >= 0
+        want[s[there, j]] = x[there]
+    uw.dispatch_rows(x, torch.from_numpy(slot).cuda(), xs)
+    torch.cuda.synchronize()
+    assert torch.equal(xs, want)
+
+
+def test_far_offsets(env):
+    """Rows past 2^31 elements: logits, activations, their copies and the experts' rows."""
+    torch, uw = env
+    rows, cols = 70000, 32768
+    wide = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([3, 65530, 65600, 69998, 69999], device="cuda")
+    logits = torch.randn((5, 8), device="cuda").to(torch.bfloat16)
+    wide[at, cols - 8:] = logits
+    e, w = torch.empty((rows, 2), dtype=torch.int32, device="cuda"), torch.empty((rows, 2), device="cuda")
+    print("far offsets: route", flush=True)
+    uw.route(wide[:, cols - 8:], e, w)
+    want, _ = routing.route(logits.float().cpu().numpy(), 2)
+    assert np.array_equal(e[at].cpu().numpy(), want) and (e[10].cpu().numpy() == [0, 1]).all()
+    # dispatch from far rows to far rows and back
+    slot = torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")
+    slot[at, 0] = torch.tensor([69999, 5, 69000, 66000, 0], dtype=torch.int32, device="cuda")
+    wide[at] = torch.randn((5, cols), device="cuda").to(torch.bfloat16)
+    xs = torch.zeros_like(wide)
+    print("far offsets: dispatch", flush=True)
+    uw.dispatch_rows(wide, slot, xs)
+    torch.cuda.synchronize()
+    assert torch.equal(xs[slot[at, 0].long()], wide[at]) and int((xs != 0).any(dim=1).sum()) == 5
+    del xs
+    ys = torch.full((rows, cols), float("nan"), device="cuda")
+    ys[slot[at, 0].long()] = wide[at].float()
+    weights = torch.full((rows, 1), 2.0, device="cuda")
+    y = torch.empty((rows, cols), device="cuda", dtype=torch.bfloat16)
+    print("far offsets: combine", flush=True)
+    uw.combine_rows(ys, slot, weights, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y[at].float(), wide[at].float() * 2) and int((y != 0).any(dim=1).sum()) == 5
 
 
 # ---- together, on another stream and in a graph ----

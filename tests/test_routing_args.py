@@ -29,7 +29,7 @@ def route(logits=A, type=0, ld=8, tokens=4, bias=None, config=None, experts=B, w
     (dict(tokens=-1), uw.ERR_INVALID_ARG), (dict(tokens=HUGE), uw.ERR_INVALID_ARG),
     (dict(type=2), uw.ERR_INVALID_ARG), (dict(ld=7), uw.ERR_SHAPE), (dict(logits=A + 2), uw.ERR_INVALID_ARG),
     (dict(bias=A + 1), uw.ERR_INVALID_ARG), (dict(experts=A + 16), uw.ERR_INVALID_ARG),
-    (dict(weights=B + 4), uw.ERR_INVALID_ARG),
+    (dict(weights=B + 4), uw.ERR_INVALID_ARG), (dict(bias=D + 8), uw.ERR_INVALID_ARG),
     (dict(config=cfg(experts=0)), uw.ERR_SHAPE), (dict(config=cfg(experts=1025), ld=2000), uw.ERR_SHAPE),
     (dict(config=cfg(top_k=0)), uw.ERR_INVALID_ARG), (dict(config=cfg(top_k=9)), uw.ERR_INVALID_ARG),
     (dict(config=cfg(experts=128, top_k=65), ld=128), uw.ERR_INVALID_ARG),
