@@ -126,8 +126,8 @@ def _load() -> C.CDLL:
         "uw_lora_plan_bytes": ([i64, i32], C.c_size_t),
         "uw_lora_plan": ([vp, i64, i32, vp, C.c_size_t, vp], st),
         "uw_lora_workspace_bytes": ([C.POINTER(vp), i32, i64], C.c_size_t),
-        "uw_lora_apply": ([C.POINTER(vp), i32, vp, C.c_size_t, vp, i64, C.POINTER(vp), C.POINTER(i64), C.POINTER(vp),
-                           C.POINTER(i64), i64, vp, C.c_size_t, vp], st),
+        # (its five arrays are passed by address: one block of memory holds them)
+        "uw_lora_apply": ([vp, i32, vp, C.c_size_t, vp, i64, vp, vp, vp, vp, i64, vp, C.c_size_t, vp], st),
         "uw_stream_create": ([i32, i32, C.POINTER(vp)], st),
         "uw_stream_destroy": ([vp], st),
         "uw_device_cu_count": ([], i32),
@@ -586,8 +586,7 @@ class Adapters:
             pass
 
 
-_VP = [C.c_void_p * n for n in range(5)]
-_I64 = [C.c_int64 * n for n in range(5)]
+_LORA_BLOCK = [C.c_int64 * (5 * n) for n in range(5)]  # handles, bases, their strides, outputs, theirs
 
 
 def lora_plan_bytes(tokens: int, slots: int) -> int:
@@ -622,17 +621,18 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
     xp, ldx = _rows(x, "x", _bf16, (t, adapters[0].cols), dev)
     hs, yp, ldy, bp, ldb = [], [], [], [], []
     for a, y, b in zip(adapters, ys, bases):
-        hs.append(a._h.value)
+        hs.append(a._h.value or 0)
         shape = (t, a.rows)
         p, ld = _rows(y, "ys", _f32, shape, dev)
         yp.append(p)
         ldy.append(ld)
         if b is not y:
-            p, ld = (None, 0) if b is None else _rows(b, "bases", _f32, shape, dev)
+            p, ld = (0, 0) if b is None else _rows(b, "bases", _f32, shape, dev)
         bp.append(p)
         ldb.append(ld)
-    vp, i64 = _VP[n], _I64[n]
     pp, pb = _bytes(plan, "plan", dev)
     wp, wb = _bytes(work, "work", dev)
-    _check(_lib.uw_lora_apply(vp(*hs), n, pp, pb, xp, ldx, vp(*bp), i64(*ldb), vp(*yp), i64(*ldy), t, wp, wb,
+    block = _LORA_BLOCK[n](*hs, *bp, *ldb, *yp, *ldy)
+    at, step = C.addressof(block), 8 * n
+    _check(_lib.uw_lora_apply(at, n, pp, pb, xp, ldx, at + step, at + 2 * step, at + 3 * step, at + 4 * step, t, wp, wb,
                               _stream_ptr(stream)))

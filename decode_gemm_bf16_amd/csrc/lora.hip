@@ -34,7 +34,8 @@ constexpr int kLoraMaxSplit = 8;
 // saved is 2.3 us of host time more.)
 constexpr int64_t kLoraOneBytes = 256 << 10;
 
-__device__ __forceinline__ bool plan_has(const LoraArgs& a, int tile) {
+template <typename Args>
+__device__ __forceinline__ bool plan_has(const Args& a, int tile) {
   return a.header->tokens == a.tokens && a.header->slots == a.slots && tile < a.header->tiles;
 }
 
@@ -55,8 +56,8 @@ union ShrinkLds {
 // of a memory page's activation.  The waves' sums are added in LDS.
 // Bound by what a CU takes in at memory latency, about 22 GB/s each, so the work
 // is spread over all of them before anything else.
-template <int NS, int NR>
-__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile, int kpart,
+template <int NS, int NR, typename Args>
+__device__ __forceinline__ void shrink_tile(const Args& a, const LoraProj& p, const PlanTile& tile, int kpart,
                                             int ksplit, int rblock, int nr, ShrinkLds& lds, float* out, int64_t ldout) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int batches = a.cols / 64, per = (batches + ksplit - 1) / ksplit;
@@ -122,7 +123,8 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const LoraProj& p
   }
 }
 
-__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_shrink_kernel(LoraArgs a) {
+template <int N>
+__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_shrink_kernel(LoraArgsOf<N> a) {
   __shared__ __attribute__((aligned(16))) ShrinkLds lds;
   const LoraProj& p = a.proj[blockIdx.z % a.nproj];
   const int rblock = blockIdx.z / a.nproj, kpart = blockIdx.x;
@@ -218,8 +220,8 @@ __device__ __forceinline__ void stage_parts(const LoraSource& from, int len, int
 // is token q + 4 k of 16, so that up to 4 KM tokens take the first KM of a lane's
 // 4 results.  B lies in the order of the operands: a lane's 4 x 4 values of a
 // group and rank block are 32 bytes.
-template <int NS, int KM, int C, bool STREAM, int WAVES>
-__device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p, const PlanTile& tile,
+template <int NS, int KM, int C, bool STREAM, int WAVES, typename Args>
+__device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, const PlanTile& tile,
                                             const LoraSource& from, int reps, LoraParts& parts) {
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int groups = (p.rows + 63) / 64;
@@ -321,8 +323,8 @@ __device__ __forceinline__ void expand_tile(const LoraArgs& a, const LoraProj& p
 
 // C: groups of 64 rows per wave; two at once where the tile has at most 4
 // tokens.  STREAM: y passes the caches by.
-template <int C, bool STREAM>
-__global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraArgs a) {
+template <int N, int C, bool STREAM>
+__global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraArgsOf<N> a) {
   __shared__ __attribute__((aligned(16))) LoraParts parts;
   const LoraProj& p = a.proj[blockIdx.z];
   if (!plan_has(a, blockIdx.y)) return;
@@ -343,7 +345,8 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
 // Each workgroup takes 512 rows of B and makes the products with A for itself:
 // A is read rows / 512 times over, from L2 but for the first, and a launch is
 // saved.
-__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgs a) {
+template <int N>
+__global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgsOf<N> a) {
   __shared__ __attribute__((aligned(16))) union {
     ShrinkLds lds;
     LoraParts parts;
@@ -367,13 +370,54 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgs
   expand_tile<1, 1, 1, false, kShrinkWaves>(a, p, tile, LoraSource{v[0], kRankBlock, 0, 1}, 1, u.parts);
 }
 
-template <int C>
-void launch_expand(const LoraArgs& a, int rows, hipStream_t s) {
+template <int N, int C>
+void launch_expand(const LoraArgsOf<N>& a, int rows, hipStream_t s) {
   const dim3 grid((rows + 256 * C - 1) / (256 * C), a.tiles_max, a.nproj);
   if (a.stream)
-    hipLaunchKernelGGL((lora_expand_kernel<C, true>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((lora_expand_kernel<N, C, true>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((lora_expand_kernel<C, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((lora_expand_kernel<N, C, false>), grid, dim3(256), 0, s, a);
+}
+
+template <int N>
+hipError_t launch_apply(const LoraArgs& all, hipStream_t s) {
+  LoraArgsOf<N> a;
+  int rank16 = 0, rows = 0;
+  for (int i = 0; i < N; ++i) {
+    a.proj[i] = all.proj[i];
+    rank16 = a.proj[i].rank16 > rank16 ? a.proj[i].rank16 : rank16;  // (those past nproj are zeros)
+    rows = a.proj[i].rows > rows ? a.proj[i].rows : rows;
+  }
+  a.header = all.header;
+  a.tiles = all.tiles;
+  a.order = all.order;
+  a.x = all.x;
+  a.ldx = all.ldx;
+  a.tokens = all.tokens;
+  a.slots = all.slots;
+  a.cols = all.cols;
+  a.nproj = all.nproj;
+  a.ksplit = all.ksplit;
+  a.tiles_max = all.tiles_max;
+  a.halves = all.halves;
+  a.stream = all.stream;
+  if (a.tokens <= 4 && rank16 <= kRankBlock && (int64_t)rank16 * a.cols * 2 <= kLoraOneBytes) {
+    hipLaunchKernelGGL(lora_one_kernel<N>, dim3((rows + 511) / 512, a.tiles_max, a.nproj), dim3(64 * kShrinkWaves), 0,
+                       s, a);
+    return hipGetLastError();
+  }
+  const unsigned rblocks = (rank16 + kRankBlock - 1) / kRankBlock;
+  hipLaunchKernelGGL(lora_shrink_kernel<N>, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),
+                     dim3(64 * kShrinkWaves), 0, s, a);
+  // Few tokens a slot: mostly tiles of a token or a few, whose workgroups take 1024
+  // columns (64 adapters of one token, gate and up of 14336 rows: 17.8 us against
+  // 33.3 with 256; 256 tokens of one adapter in 256 slots, which it does not suit,
+  // 20.5 against 14.7), if there are workgroups enough
+  if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
+    launch_expand<N, 4>(a, rows, s);
+  else
+    launch_expand<N, 1>(a, rows, s);
+  return hipGetLastError();
 }
 
 // ---- loading an adapter into a slot ----
@@ -421,24 +465,7 @@ int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj) {
 }
 
 hipError_t launch_lora_apply(const LoraArgs& a, hipStream_t s) {
-  int rank16 = 0, rows = 0;
-  for (int i = 0; i < a.nproj; ++i) {
-    rank16 = a.proj[i].rank16 > rank16 ? a.proj[i].rank16 : rank16;
-    rows = a.proj[i].rows > rows ? a.proj[i].rows : rows;
-  }
-  if (a.tokens <= 4 && rank16 <= kRankBlock && (int64_t)rank16 * a.cols * 2 <= kLoraOneBytes) {
-    hipLaunchKernelGGL(lora_one_kernel, dim3((rows + 511) / 512, a.tiles_max, a.nproj), dim3(64 * kShrinkWaves), 0, s,
-                       a);
-    return hipGetLastError();
-  }
-  const unsigned rblocks = (rank16 + kRankBlock - 1) / kRankBlock;
-  hipLaunchKernelGGL(lora_shrink_kernel, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),
-                     dim3(64 * kShrinkWaves), 0, s, a);
-  if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
-    launch_expand<4>(a, rows, s);
-  else
-    launch_expand<1>(a, rows, s);
-  return hipGetLastError();
+  return a.nproj == 1 ? launch_apply<1>(a, s) : a.nproj == 2 ? launch_apply<2>(a, s) : launch_apply<kLoraMaxProj>(a, s);
 }
 
 hipError_t launch_lora_load(const uint16_t* a, const uint16_t* b, int64_t rows, int64_t cols, int32_t rank,

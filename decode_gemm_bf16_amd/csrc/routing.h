@@ -79,8 +79,11 @@ struct LoraProj {
   int32_t rows, rank16;
   float* part;  // [ksplit][tokens][rank16] products with A
 };
-struct LoraArgs {
-  LoraProj proj[kLoraMaxProj];
+// N: projections that there is room for (a launch costs about 0.4 us of host time
+// more per 100 bytes of arguments).
+template <int N>
+struct LoraArgsOf {
+  LoraProj proj[N];
   const PlanHeader* header;
   const PlanTile* tiles;
   const int32_t* order;
@@ -90,6 +93,7 @@ struct LoraArgs {
   bool halves;  // the shrink takes 32 tokens a workgroup
   bool stream;  // y passes the caches by
 };
+using LoraArgs = LoraArgsOf<kLoraMaxProj>;
 // Rules on sizes alone.
 bool lora_halves(int64_t tokens, int32_t slots, int nproj);
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj);
