@@ -1,5 +1,8 @@
 """Routing of tokens to experts and back, and low-rank adapters, in float64.
 
+TEST INFRASTRUCTURE, NOT PRODUCT CODE: imported only by tests/; shares no code
+with the library.
+
 Plain numpy, one token after the other, from the definitions:
 
 * route: score s = softmax(l) or 1 / (1 + exp(-l)); choice c = s + bias, or l
