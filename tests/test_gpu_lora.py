@@ -214,6 +214,71 @@ def test_far_offsets(env):
     assert not y[rest].any()
 
 
+def test_most_tokens_and_slots(env):
+    """2^20 tokens over 4000 slots, most of them empty: every tile of the plan."""
+    torch, uw = env
+    rng = np.random.default_rng(25)
+    tokens, slots, rows, cols = 1 << 20, 4000, 16, 64
+    ranks = np.zeros(slots, dtype=int)
+    ranks[::500] = 3
+    s = Setup(env, rng, slots, rows, cols, 3, ranks)
+    index = rng.integers(-1, slots, size=tokens)
+    d = torch.from_numpy(index.astype(np.int32)).cuda()
+    x = torch.randn((tokens, cols), device="cuda").to(torch.bfloat16)
+    base = torch.randn((tokens, rows), device="cuda")
+    y = torch.full_like(base, NAN)
+    plan = torch.empty(uw.lora_plan_bytes(tokens, slots), dtype=torch.uint8, device="cuda")
+    work = torch.empty(uw.lora_workspace_bytes([s.h], tokens), dtype=torch.uint8, device="cuda")
+    print("lora 2^20 tokens, 4000 slots", flush=True)
+    uw.lora_plan(d, slots, plan)
+    uw.lora_apply([s.h], plan, x, [y], work, bases=[base])
+    torch.cuda.synchronize()
+    some = np.isin(index, list(s.values))
+    none = torch.from_numpy(~some).cuda()
+    assert torch.equal(y[none], base[none])
+    at = np.nonzero(some)[0]
+    assert len(at) > 1000
+    where = torch.from_numpy(at).cuda()
+    check(y[where].cpu().numpy().astype(np.float64), x[where].double().cpu().numpy(), index[at], s.values,
+          base[where].cpu().numpy())
+
+
+def test_no_bases_and_a_captured_load(env):
+    """The C call without bases writes the adapters' part alone; a load that is
+    captured takes what its sources hold at each replay."""
+    import ctypes as C
+    torch, uw = env
+    rng = np.random.default_rng(26)
+    tokens, rows, cols = 50, 80, 128
+    s = Setup(env, rng, 2, rows, cols, 8, [0, 0])
+    x, xv = values(rng, tokens, cols)
+    xd = uw.bf16_tensor(x)
+    index = rng.integers(-1, 2, size=tokens)
+    d = torch.from_numpy(index.astype(np.int32)).cuda()
+    plan = torch.empty(uw.lora_plan_bytes(tokens, 2), dtype=torch.uint8, device="cuda")
+    work = torch.empty(uw.lora_workspace_bytes([s.h], tokens), dtype=torch.uint8, device="cuda")
+    a, b = torch.zeros((5, cols), dtype=torch.bfloat16, device="cuda"), torch.zeros((rows, 5), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((tokens, rows), device="cuda")
+    uw.lora_plan(d, 2, plan)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st = torch.cuda.current_stream()
+        s.h.load(1, a, b, 0.25, stream=st)
+        uw._check(uw._lib.uw_lora_apply((C.c_void_p * 1)(s.h.handle), 1, plan.data_ptr(), plan.numel(), xd.data_ptr(), cols,
+                                        None, None, (C.c_void_p * 1)(y.data_ptr()), (C.c_int64 * 1)(rows), tokens,
+                                        work.data_ptr(), work.numel(), st.cuda_stream))
+    for _ in range(3):
+        ab, av = values(rng, 5, cols)
+        bb, bv = values(rng, rows, 5)
+        a.copy_(uw.bf16_tensor(ab))
+        b.copy_(uw.bf16_tensor(bb))
+        y.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(y.cpu().numpy().astype(np.float64), xv, index, {1: (av, bv, 0.25)}, np.zeros((tokens, rows), dtype=np.float32))
+
+
 def test_two_streams_share_a_plan(env):
     torch, uw = env
     rng = np.random.default_rng(24)
@@ -484,6 +549,42 @@ def test_moe_layer(env, tokens, pipelines):
     uw.moe_forward(mats, pipelines, torch.full((tokens, experts), -INF, device="cuda"), uw.bf16_tensor(xb), y, work, k)
     torch.cuda.synchronize()
     assert (y == 0).all()
+
+
+def test_moe_layer_on_its_stream(env):
+    """On the experts' own stream, behind work that is queued there."""
+    torch, uw = env
+    rng = np.random.default_rng(27)
+    tokens, hidden, inter, experts = 24, 128, 128, 4
+    ws = [[synth.weights(r, c, 900 + 3 * e + j, 0.002, 10) for j, (r, c) in
+           enumerate(((inter, hidden), (inter, hidden), (hidden, inter)))] for e in range(experts)]
+    mats = [uw.Matrix(w, uw.FMT_PALETTE) for three in ws for w in three]
+    side = torch.cuda.Stream()
+    for m in mats:
+        m.set_streams(side)
+    xb, _ = values(rng, tokens, hidden)
+    xd, logits = uw.bf16_tensor(xb), torch.from_numpy(rng.standard_normal((tokens, experts), dtype=np.float32)).cuda()
+    work = torch.empty(uw.moe_workspace_bytes(tokens, hidden, inter, experts, 2), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x, l = torch.zeros_like(xd), torch.zeros_like(logits)
+        big = torch.ones(1 << 26, device="cuda")
+        for _ in range(10):
+            big.mul_(1.0001)
+        x.copy_(xd)
+        l.copy_(logits)
+        y = torch.zeros((tokens, hidden), device="cuda")
+        uw.moe_forward(mats, [4, 4, 4], l, x, y, work, 2)
+        y2 = y * 2  # and what is queued behind sees the result
+    torch.cuda.synchronize()
+    chosen, weights = routing.route(logits.cpu().numpy(), 2)
+    want = np.zeros((tokens, hidden))
+    for t in range(tokens):
+        for e, w in zip(chosen[t], weights[t]):
+            want[t] += w * oracle.mlp_layer_fp64(xb[t:t + 1], *ws[e])[3][0]
+    assert oracle.rel_err(y2.cpu().numpy() / 2, want) <= 1e-3
+    for m in mats:
+        m.free()
 
 
 def test_moe_layer_refuses_capture(env):

@@ -397,6 +397,57 @@ def test_far_offsets(env):
     assert torch.equal(y[at].float(), wide[at].float() * 2) and int((y != 0).any(dim=1).sum()) == 5
 
 
+def test_most_tokens(env):
+    """The largest token counts: 2^24 routed, and more dispatched and combined than
+    one grid has workgroups along the tokens."""
+    torch, uw = env
+    t = 1 << 24
+    logits = torch.randn((t, 3), device="cuda")
+    e, w = torch.empty((t, 1), dtype=torch.int32, device="cuda"), torch.empty((t, 1), device="cuda")
+    print("route 2^24 tokens", flush=True)
+    uw.route(logits, e, w, renormalise=False)
+    top, at = torch.softmax(logits.double(), dim=1).max(dim=1)
+    assert torch.equal(e[:, 0].long(), at)  # (float32 normals: no equal logits where the largest decides)
+    assert float(((w[:, 0].double() - top).abs() / top).max()) <= WEIGHT_TOL
+    del logits, top, at, e, w
+    t = (1 << 20) + 1000
+    x = torch.randn((t, 8), device="cuda").to(torch.bfloat16)
+    slot = torch.randperm(t, device="cuda").to(torch.int32).reshape(t, 1)
+    xs = torch.empty_like(x)
+    print("dispatch and combine 2^20 + 1000 tokens", flush=True)
+    uw.dispatch_rows(x, slot, xs)
+    torch.cuda.synchronize()
+    assert torch.equal(xs[slot[:, 0].long()], x)
+    y = torch.empty((t, 8), device="cuda")
+    uw.combine_rows(xs.float(), slot, torch.full((t, 1), 0.5, device="cuda"), y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, x.float() * 0.5)
+
+
+def test_group_in_a_graph(env):
+    """Both forms of the sort captured, replayed over new labels."""
+    torch, uw = env
+    for n, groups in ((3000, 40), (30000, 300)):
+        d = torch.zeros(n, dtype=torch.int32, device="cuda")
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device="cuda")
+        order, slot = torch.empty_like(d), torch.empty_like(d)
+        work = torch.empty(uw.group_rows_workspace_bytes(n, groups), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            uw.group_rows(d, groups, offsets, order, slot, work, stream=torch.cuda.current_stream())
+        for seed in range(4):
+            index = np.random.default_rng(seed).integers(-1, groups, size=n)
+            d.copy_(torch.from_numpy(index.astype(np.int32)))
+            for b in (offsets, order, slot, work):
+                b.fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            label = np.where(index < 0, groups, index)
+            want = np.argsort(label, kind="stable")
+            assert np.array_equal(order.cpu().numpy(), want)
+            assert np.array_equal(offsets.cpu().numpy(), np.searchsorted(label[want], np.arange(groups + 1)))
+
+
 # ---- together, on another stream and in a graph ----
 
 
