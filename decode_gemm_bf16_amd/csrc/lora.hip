@@ -211,16 +211,15 @@ __device__ __forceinline__ void stage_parts(const LoraSource& from, int len, int
   }
 }
 
-// One workgroup: one tile; each of its WAVES waves takes C groups of 64 rows of B
-// (WAVES apart) at once, `reps` times over, and 16 NS tokens at a time.  v is
-// the A operand (16 tokens x 16 ranks) and B the B operand; row 4 r + j of a
-// group is column r of its j-th 16-column product, so that a lane's results of
-// the four products are 4 neighbouring columns of y, and a load or store of 16
-// bytes a lane covers 256 bytes of each of 4 tokens.  Row 4 q + k of the A operand
-// is token q + 4 k of 16, so that up to 4 KM tokens take the first KM of a lane's
-// 4 results.  B lies in the order of the operands: a lane's 4 x 4 values of a
-// group and rank block are 32 bytes.
-template <int NS, int KM, int C, bool STREAM, int WAVES, typename Args>
+// One workgroup: one tile; each of its 4 waves takes one group of 64 rows of B,
+// `reps` times over, and 16 NS tokens at a time.  v is the A operand (16 tokens x
+// 16 ranks) and B the B operand; row 4 r + j of a group is column r of its j-th
+// 16-column product, so that a lane's results of the four products are 4
+// neighbouring columns of y, and a load or store of 16 bytes a lane covers 256
+// bytes of each of 4 tokens.  Row 4 q + k of the A operand is token q + 4 k of 16.
+// B lies in the order of the operands: a lane's 4 x 4 values of a group and rank
+// block are 32 bytes.
+template <int NS, bool STREAM, typename Args>
 __device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, const PlanTile& tile,
                                             const LoraSource& from, int reps, LoraParts& parts) {
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -231,46 +230,38 @@ __device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, co
   const int nr = (entry.rank + 15) / 16;
   for (int rep = 0; rep < reps; ++rep)
     for (int i0 = 0; i0 < tile.len; i0 += 16 * NS) {
-      const int g0 = (blockIdx.x * reps + rep) * WAVES * C + w;
-      int tok[NS][KM];
+      const int g = (blockIdx.x * reps + rep) * 4 + w;
+      // columns past the last row of B read the last four: no branch between the loads
+      const int n = g * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4, gc = g < groups ? g : groups - 1;
+      int tok[NS][4];
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int k = 0; k < KM; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const int t = i0 + i * 16 + q + 4 * k;  // past the tile's end: its last token, not stored
           tok[i][k] = a.order[tile.start + (t < tile.len ? t : tile.len - 1)];
         }
-      u32x4 bv[C][2];
+      u32x4 bv[2];
       auto load_b = [&](int rb) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int g = g0 + WAVES * c < groups ? g0 + WAVES * c : groups - 1;
-          const u32x4* src = (const u32x4*)(b + ((int64_t)rb * groups + g) * 1024);
-          bv[c][0] = src[0];
-          bv[c][1] = src[1];
-        }
+        const u32x4* src = (const u32x4*)(b + ((int64_t)rb * groups + gc) * 1024);
+        bv[0] = src[0];
+        bv[1] = src[1];
       };
       if (nr > 0) load_b(0);
-      f32x4 acc[C][NS][4] = {};
+      f32x4 acc[NS][4] = {};
       if (p.base) {
-        // columns past the last row of B read the last four: no branch between the loads
-        f32x4 v[C][NS][KM];
+        f32x4 v[NS][4];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int n = (g0 + WAVES * c) * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4;
+        for (int i = 0; i < NS; ++i)
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
+          for (int k = 0; k < 4; ++k)
+            v[i][k] = __builtin_nontemporal_load((const f32x4*)(p.base + (int64_t)tok[i][k] * p.ldbase + nc));
 #pragma unroll
-            for (int k = 0; k < KM; ++k) v[c][i][k] = __builtin_nontemporal_load((const f32x4*)(p.base + (int64_t)tok[i][k] * p.ldbase + nc));
-        }
+        for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
-#pragma unroll
-            for (int k = 0; k < KM; ++k)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[c][i][j][k] = v[c][i][k][j];
+            for (int j = 0; j < 4; ++j) acc[i][j][k] = v[i][k][j];
       }
       for (int r0 = 0; r0 < nr; r0 += kRankBlock / 16) {
         const int blocks = nr - r0 < kRankBlock / 16 ? nr - r0 : kRankBlock / 16;
@@ -280,12 +271,10 @@ __device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, co
           __syncthreads();
         }
         for (int rb = 0; rb < blocks; ++rb) {
-          s16x4 now[C][4];
+          s16x4 now[4];
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              now[c][j] = __builtin_bit_cast(s16x4, u32x2{bv[c][j >> 1][(j & 1) * 2], bv[c][j >> 1][(j & 1) * 2 + 1]});
+          for (int j = 0; j < 4; ++j)
+            now[j] = __builtin_bit_cast(s16x4, u32x2{bv[j >> 1][(j & 1) * 2], bv[j >> 1][(j & 1) * 2 + 1]});
           if (r0 + rb + 1 < nr) load_b(r0 + rb + 1);
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
@@ -294,31 +283,112 @@ __device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, co
               // tokens past the tile's end: stale LDS, in rows of the result that are not stored
               const s16x4 vv = *(const s16x4*)&parts[h][i0 + i * 16 + (r >> 2) + 4 * (r & 3)][rb * 16 + 4 * q];
 #pragma unroll
-              for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  acc[c][i][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vv, now[c][j], acc[c][i][j], 0, 0, 0);
+              for (int j = 0; j < 4; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vv, now[j], acc[i][j], 0, 0, 0);
             }
           }
         }
       }
 #pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + i * 16 + q + 4 * k < tile.len && n < p.rows) {
+            const f32x4 v = {acc[i][0][k], acc[i][1][k], acc[i][2][k], acc[i][3][k]};
+            f32x4* to = (f32x4*)(p.y + (int64_t)tok[i][k] * p.ldy + n);
+            if constexpr (STREAM)
+              __builtin_nontemporal_store(v, to);
+            else
+              *to = v;
+          }
+    }
+}
+
+// The same for a tile of at most 4 tokens, whose token t is row 4 t of the A
+// operand, by WAVES waves with C groups (WAVES apart) at once.  Each wave cuts v
+// into its parts by itself, in the registers of that operand, and waits for no
+// other: 64 adapters of one token, gate and up of 14336 rows, 16.3 us against 17.8
+// with the parts in LDS.  (Of 4 groups a wave, 2 at once: 4 at once take 27.6 us,
+// one after the other 19.5.)
+template <int C, bool STREAM, int WAVES, typename Args>
+__device__ __forceinline__ void expand_few(const Args& a, const LoraProj& p, const PlanTile& tile,
+                                           const LoraSource& from, int reps) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int groups = (p.rows + 63) / 64;
+  const uint16_t* b = p.b + (int64_t)(tile.slot < 0 ? 0 : tile.slot) * p.rank16 * groups * 64 + lane * 16;
+  const LoraSlot entry = tile.slot >= 0 ? p.table[tile.slot] : LoraSlot{0, 0.f};
+  if (entry.rank == 0 && p.base == p.y && p.ldbase == p.ldy) return;  // in place, nothing to add
+  const int nr = (entry.rank + 15) / 16;
+  // results: lane (q, r) has columns 4 r .. + 3 of a group for token q (past the tile's end: its last, not stored)
+  const int tok = a.order[tile.start + (q < tile.len ? q : tile.len - 1)];
+  const int mine = (r & 3) == 0 && (r >> 2) < tile.len ? r >> 2 : -1;  // the operand's token
+  const float* v0 = from.v + (mine < 0 ? 0 : mine) * from.ld + 4 * q;
+  for (int rep = 0; rep < reps; ++rep) {
+    const int g0 = (blockIdx.x * reps + rep) * WAVES * C + w;
+    u32x4 bv[C][2];
+    f32x4 v;
+    auto load = [&](int rb) {
+#pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int n = (g0 + WAVES * c) * 64 + 4 * r;
+        const int g = g0 + WAVES * c < groups ? g0 + WAVES * c : groups - 1;
+        const u32x4* src = (const u32x4*)(b + ((int64_t)rb * groups + g) * 1024);
+        bv[c][0] = src[0];
+        bv[c][1] = src[1];
+      }
+      v = *(const f32x4*)(v0 + rb * 16);
+      for (int s = 1; s < from.ksplit; ++s) v += *(const f32x4*)(v0 + rb * 16 + s * from.next);
+    };
+    f32x4 acc[C][4] = {};
+    if (p.base) {
+      // columns past the last row of B read the last four: no branch between the loads
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
+      for (int c = 0; c < C; ++c) {
+        const int n = (g0 + WAVES * c) * 64 + 4 * r, nc = n < p.rows ? n : p.rows - 4;
+        const f32x4 y = __builtin_nontemporal_load((const f32x4*)(p.base + (int64_t)tok * p.ldbase + nc));
 #pragma unroll
-          for (int k = 0; k < KM; ++k)
-            if (i0 + i * 16 + q + 4 * k < tile.len && n < p.rows) {
-              const f32x4 v = {acc[c][i][0][k], acc[c][i][1][k], acc[c][i][2][k], acc[c][i][3][k]};
-              f32x4* to = (f32x4*)(p.y + (int64_t)tok[i][k] * p.ldy + n);
-              if constexpr (STREAM)
-                __builtin_nontemporal_store(v, to);
-              else
-                *to = v;
-            }
+        for (int j = 0; j < 4; ++j) acc[c][j][0] = y[j];
       }
     }
+    if (nr > 0) load(0);
+    for (int rb = 0; rb < nr; ++rb) {
+      uint16_t h[3][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // ranks past the adapter's own: an infinity in x makes NaN of them
+        float f = mine >= 0 && rb * 16 + 4 * q + j < entry.rank ? v[j] * entry.scale : 0.f;
+#pragma unroll
+        for (int m = 0; m < 3; ++m) h[m][j] = bf16_part(f);
+      }
+      s16x4 now[C][4];
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          now[c][j] = __builtin_bit_cast(s16x4, u32x2{bv[c][j >> 1][(j & 1) * 2], bv[c][j >> 1][(j & 1) * 2 + 1]});
+      if (rb + 1 < nr) load(rb + 1);
+#pragma unroll
+      for (int m = 2; m >= 0; --m) {  // the smallest part first
+        const s16x4 vv = __builtin_bit_cast(s16x4, u32x2{h[m][0] | (uint32_t)h[m][1] << 16, h[m][2] | (uint32_t)h[m][3] << 16});
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vv, now[c][j], acc[c][j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int n = (g0 + WAVES * c) * 64 + 4 * r;
+      if (q < tile.len && n < p.rows) {
+        const f32x4 y = {acc[c][0][0], acc[c][1][0], acc[c][2][0], acc[c][3][0]};
+        f32x4* to = (f32x4*)(p.y + (int64_t)tok * p.ldy + n);
+        if constexpr (STREAM)
+          __builtin_nontemporal_store(y, to);
+        else
+          *to = y;
+      }
+    }
+  }
 }
 
 // C: groups of 64 rows per wave; two at once where the tile has at most 4
@@ -333,11 +403,11 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
   constexpr int kFew = C > 2 ? 2 : C;
   const LoraSource from{p.part + (int64_t)tile.start * p.rank16, p.rank16, (int64_t)a.tokens * p.rank16, a.ksplit};
   if (tile.len <= 4)
-    expand_tile<1, 1, kFew, STREAM, 4>(a, p, tile, from, C / kFew, parts);
+    expand_few<kFew, STREAM, 4>(a, p, tile, from, C / kFew);
   else if (C > 1 || tile.len <= 32)
-    expand_tile<2, 4, 1, STREAM, 4>(a, p, tile, from, C, parts);
+    expand_tile<2, STREAM>(a, p, tile, from, C, parts);
   else
-    expand_tile<4, 4, 1, STREAM, 4>(a, p, tile, from, C, parts);
+    expand_tile<4, STREAM>(a, p, tile, from, C, parts);
 }
 
 // ---- both in one launch, for at most four tokens ----
@@ -347,10 +417,7 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
 // saved.
 template <int N>
 __global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgsOf<N> a) {
-  __shared__ __attribute__((aligned(16))) union {
-    ShrinkLds lds;
-    LoraParts parts;
-  } u;
+  __shared__ __attribute__((aligned(16))) ShrinkLds lds;
   __shared__ __attribute__((aligned(16))) float v[4][kRankBlock];
   const LoraProj& p = a.proj[blockIdx.z];
   if (!plan_has(a, blockIdx.y)) return;
@@ -361,13 +428,13 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 4) void lora_one_kernel(LoraArgs
   tile.len = __builtin_amdgcn_readfirstlane(tile.len);
   const int nr = tile.slot < 0 ? 0 : __builtin_amdgcn_readfirstlane((p.table[tile.slot].rank + 15) / 16);
   if (nr == 1)
-    shrink_tile<1, 1>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+    shrink_tile<1, 1>(a, p, tile, 0, 1, 0, nr, lds, v[0], kRankBlock);
   else if (nr == 2)
-    shrink_tile<1, 2>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+    shrink_tile<1, 2>(a, p, tile, 0, 1, 0, nr, lds, v[0], kRankBlock);
   else if (nr > 2)
-    shrink_tile<1, 4>(a, p, tile, 0, 1, 0, nr, u.lds, v[0], kRankBlock);
+    shrink_tile<1, 4>(a, p, tile, 0, 1, 0, nr, lds, v[0], kRankBlock);
   __syncthreads();
-  expand_tile<1, 1, 1, false, kShrinkWaves>(a, p, tile, LoraSource{v[0], kRankBlock, 0, 1}, 1, u.parts);
+  expand_few<1, false, kShrinkWaves>(a, p, tile, LoraSource{v[0], kRankBlock, 0, 1}, 1);
 }
 
 template <int N, int C>
@@ -410,8 +477,8 @@ hipError_t launch_apply(const LoraArgs& all, hipStream_t s) {
   hipLaunchKernelGGL(lora_shrink_kernel<N>, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),
                      dim3(64 * kShrinkWaves), 0, s, a);
   // Few tokens a slot: mostly tiles of a token or a few, whose workgroups take 1024
-  // columns (64 adapters of one token, gate and up of 14336 rows: 17.8 us against
-  // 33.3 with 256; 256 tokens of one adapter in 256 slots, which it does not suit,
+  // columns (64 adapters of one token, gate and up of 14336 rows: 16.3 us against
+  // 30.2 with 256; 256 tokens of one adapter in 256 slots, which it does not suit,
   // 20.5 against 14.7), if there are workgroups enough
   if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
     launch_expand<N, 4>(a, rows, s);
