@@ -22,14 +22,19 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {  // round to nearest even
 // position is its counter plus its rank among the equal labels of the 64.  No
 // position depends on the order in which atomics are served.
 //
+// A lane reads kKept entries at once and keeps its section's first kKept from the
+// counting to the placing, so that most sections are read once.
+//
 // Up to kOneBlock entries one workgroup does all of it (in a graph, 8 and 256
-// groups: 1024 entries 4.0 and 4.9 us against 6.1 and 7.1 in two launches, 4096 6.3
-// and 8.6 against 7.3 and 8.9, 8192 9.2 and 13.2 against 7.6 and 9.4).  Beyond, a
+// groups: 1024 entries 4.1 and 4.8 us against 6.3 and 7.2 in two launches, 4096 6.1
+// and 7.6 against 7.1 and 7.9, 8192 9.1 and 12.0 against 7.2 and 8.1).  Beyond, a
 // first kernel writes each workgroup's counts and in the second each workgroup sums
-// the counts of those before it by itself.
+// the counts of those before it by itself (65536 entries 8.4 and 9.6 us, 2^21 20.9
+// and 29).
 
 constexpr int64_t kOneBlock = 4096;
 constexpr int kMaxBlocks = 256;
+constexpr int kKept = 4;
 
 // Waves of a workgroup: their counters and the labels' totals stay within 64 KB of LDS.
 int waves_of(int32_t groups) { return groups < 900 ? 16 : groups < 1700 ? 8 : groups < 3000 ? 4 : 2; }
@@ -40,12 +45,15 @@ int waves_one(int64_t n, int32_t groups) {
   return (int)(want < most ? want : most);
 }
 
-// Entries per workgroup: a multiple of 64 per wave, at most kMaxBlocks of them.
+// Entries per workgroup, a multiple of 64 per wave.  64 workgroups, because each
+// reads the counts of all; with that at least one entry a lane (16384 of 256 groups
+// 8.2 us against 9.0 with two) and at most the kKept that are read once (2^19
+// entries 15.5 us against 17.8 with two), as far as kMaxBlocks workgroups do.
 int64_t chunk_of(int64_t n, int waves) {
   const int64_t step = 64 * waves;
   if (n <= kOneBlock) return (n + step - 1) / step * step;
-  const int64_t want = (n + kMaxBlocks - 1) / kMaxBlocks, least = 2 * step;
-  const int64_t c = want > least ? want : least;
+  const int64_t want = (n + 63) / 64, most = (n + kMaxBlocks - 1) / kMaxBlocks;
+  const int64_t c = most > kKept * step ? most : want > kKept * step ? kKept * step : want;
   return (c + step - 1) / step * step;
 }
 
@@ -54,17 +62,40 @@ __device__ __forceinline__ int label_of(const GroupArgs& a, int64_t i) {
   return (uint32_t)v < (uint32_t)a.groups ? v : a.groups;
 }
 
-// Counts entries lo + t, lo + t + step, ... < hi of this thread.  Entries of one
-// label stand together in many batches (a request's tokens): a wave whose 64 are
-// equal adds them at once instead of one after the other.
-__device__ __forceinline__ void count(const GroupArgs& a, int* ctr, int64_t lo, int64_t hi, int t, int step) {
-  for (int64_t i = lo + t; i < hi; i += step) {
-    const int g = label_of(a, i), first = __builtin_amdgcn_readfirstlane(g);
-    const uint64_t there = __ballot(true);
-    if (__ballot(g == first) != there)
-      atomicAdd(&ctr[g], 1);
-    else if ((threadIdx.x & 63) == __builtin_ctzll(there))
-      atomicAdd(&ctr[g], (int)__popcll(there));
+// Labels of entries lo + t, lo + t + step, ... < hi (-1 past them).  The loads are
+// not under a condition, so that they are in flight together.
+template <int KEPT>
+__device__ __forceinline__ void labels_of(const GroupArgs& a, int64_t lo, int64_t hi, int t, int step, int (&g)[KEPT]) {
+#pragma unroll
+  for (int k = 0; k < KEPT; ++k) {
+    const int64_t i = lo + t + k * step;
+    g[k] = label_of(a, i < hi ? i : a.n - 1);
+  }
+#pragma unroll
+  for (int k = 0; k < KEPT; ++k)
+    if (lo + t + k * step >= hi) g[k] = -1;
+}
+
+// Counts them.  Entries of one label stand together in many batches (a request's
+// tokens): a wave whose entries are equal adds them at once instead of one after the
+// other.
+template <int KEPT>
+__device__ __forceinline__ void count(int* ctr, const int (&labels)[KEPT]) {
+  int g[KEPT];
+#pragma unroll
+  for (int k = 0; k < KEPT; ++k) g[k] = labels[k];
+#pragma unroll 1
+  for (int k = 0; k < KEPT; ++k) {
+    const uint64_t there = __ballot(g[0] >= 0);
+    if (there == 0) break;
+    const int from = __builtin_ctzll(there), first = __builtin_amdgcn_readlane(g[0], from);
+    if (__ballot(g[0] == first) != there) {
+      if (g[0] >= 0) atomicAdd(&ctr[g[0]], 1);
+    } else if ((int)(threadIdx.x & 63) == from) {
+      atomicAdd(&ctr[first], (int)__popcll(there));
+    }
+#pragma unroll
+    for (int m = 1; m < KEPT; ++m) g[m - 1] = g[m];
   }
 }
 
@@ -74,7 +105,11 @@ __global__ __launch_bounds__(1024) void group_count_kernel(GroupArgs a, int64_t 
   for (int g = threadIdx.x; g < labels; g += blockDim.x) ctr[g] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < a.n ? lo + chunk : a.n;
-  count(a, ctr, lo, hi, threadIdx.x, blockDim.x);
+  for (int64_t i0 = lo; i0 < hi; i0 += kKept * blockDim.x) {
+    int g[kKept];
+    labels_of(a, i0, hi, threadIdx.x, blockDim.x, g);
+    count(ctr, g);
+  }
   __syncthreads();
   for (int g = threadIdx.x; g < labels; g += blockDim.x) a.work[(int64_t)blockIdx.x * labels + g] = ctr[g];
 }
@@ -95,7 +130,7 @@ __device__ __forceinline__ int block_scan(int v, int* wsum) {
   return before + x - v;
 }
 
-template <bool MULTI>
+template <bool MULTI, int KEPT>
 __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t chunk) {
   extern __shared__ int ctr[];  // [waves][groups + 1], then each label's total, later its first position
   __shared__ int wsum[16];
@@ -105,7 +140,15 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
   __syncthreads();
   const int64_t sec = chunk / nw;
   const int64_t lo = blockIdx.x * chunk + w * sec, hi = lo + sec < a.n ? lo + sec : a.n;
-  count(a, ctr + w * labels, lo, hi, lane, 64);
+  int* const mine = ctr + w * labels;
+  int kept[KEPT];  // the section's first entries; the rest is read twice
+  labels_of(a, lo, hi, lane, 64, kept);
+  count(mine, kept);
+  for (int64_t i0 = lo + KEPT * 64; i0 < hi; i0 += KEPT * 64) {
+    int g[KEPT];
+    labels_of(a, i0, hi, lane, 64, g);
+    count(mine, g);
+  }
   __syncthreads();
   // this thread's labels: their counts over all entries and in the workgroups before
   const int per = (labels + blockDim.x - 1) / blockDim.x;
@@ -115,11 +158,26 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
     int all = 0, run = 0;
     if (MULTI) {
       const int32_t* h = a.work + g;
-#pragma unroll 16
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int v = h[(int64_t)b * labels];
+      const int blocks = gridDim.x;
+      auto add = [&](int b, int v) {
         all += v;
         run += b < (int)blockIdx.x ? v : 0;
+      };
+      int b = 0;
+      for (; b + 16 <= blocks; b += 16) {
+        int v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = h[(int64_t)(b + k) * labels];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) add(b + k, v[k]);
+      }
+      for (; b < blocks; b += 8) {  // as many loads in flight, also where fewer are left
+        int v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = h[(int64_t)(b + k < blocks ? b + k : blocks - 1) * labels];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (b + k < blocks) add(b + k, v[k]);
       }
     }
     for (int i = 0; i < nw; ++i) {
@@ -149,11 +207,9 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
   __syncthreads();
   int bits = 0;
   while ((1 << bits) < labels) ++bits;
-  int* mine = ctr + w * labels;
-  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const bool there = i < hi;
-    const int g = there ? label_of(a, i) : 0;
+  auto place = [&](int64_t i, int label) {
+    const bool there = label >= 0;
+    const int g = there ? label : 0;
     uint64_t same = __ballot(there);
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot((g >> b) & 1);
@@ -168,6 +224,15 @@ __global__ __launch_bounds__(1024) void group_place_kernel(GroupArgs a, int64_t 
     __builtin_amdgcn_wave_barrier();
     if (there && rank == 0) mine[g] += __popcll(same);
     __builtin_amdgcn_wave_barrier();
+  };
+  for (int64_t i0 = lo; i0 < hi; i0 += KEPT * 64) {
+    if (i0 > lo) labels_of(a, i0, hi, lane, 64, kept);
+#pragma unroll 1
+    for (int64_t i = i0; i < hi && i < i0 + KEPT * 64; i += 64) {
+      place(i + lane, kept[0]);
+#pragma unroll
+      for (int m = 1; m < KEPT; ++m) kept[m - 1] = kept[m];
+    }
   }
 }
 
@@ -251,12 +316,15 @@ hipError_t launch_group_rows(const GroupArgs& a, hipStream_t s) {
   const int64_t chunk = chunk_of(a.n, waves);
   const size_t lds = size_t(waves + 1) * labels * 4;
   if (one) {
-    hipLaunchKernelGGL(group_place_kernel<false>, dim3(1), dim3(64 * waves), lds, s, a, chunk);
+    if (chunk == 64 * waves)
+      hipLaunchKernelGGL((group_place_kernel<false, 1>), dim3(1), dim3(64 * waves), lds, s, a, chunk);
+    else
+      hipLaunchKernelGGL((group_place_kernel<false, kKept>), dim3(1), dim3(64 * waves), lds, s, a, chunk);
     return hipGetLastError();
   }
   const dim3 grid((unsigned)((a.n + chunk - 1) / chunk));
   hipLaunchKernelGGL(group_count_kernel, grid, dim3(64 * waves), size_t(labels) * 4, s, a, chunk);
-  hipLaunchKernelGGL(group_place_kernel<true>, grid, dim3(64 * waves), lds, s, a, chunk);
+  hipLaunchKernelGGL((group_place_kernel<true, kKept>), grid, dim3(64 * waves), lds, s, a, chunk);
   return hipGetLastError();
 }
 

@@ -247,6 +247,15 @@ def test_group_sizes(env, n, groups):
     run_group(env, index, groups)
 
 
+@pytest.mark.parametrize("groups", [3, 256, 1200, 3500])
+@pytest.mark.parametrize("n", [65535, 65537, 131073, 262144, 262145, 1048576, 1048577])
+def test_group_section_limits(env, n, groups):
+    """Where a lane's share grows from one entry to four, and past four; long runs and mixed labels."""
+    index = np.random.default_rng(n).integers(-1, groups + 1, size=n)
+    index[n // 3: n // 2] = groups - 1
+    run_group(env, index, groups)
+
+
 def test_group_values(env):
     for n in (100, 20000):
         run_group(env, np.full(n, 3), 8)
