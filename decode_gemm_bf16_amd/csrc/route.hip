@@ -266,8 +266,9 @@ __device__ __forceinline__ bool all_say(bool v) {
 // one step; the lanes that owned a step are counted.)
 // Errors: a sigmoid in float32 is within 4 x 2^-24 (v_exp at 1 ulp and its rounded
 // argument, both of which reach s by s (1 - s): 0.5 and 0.3; 1 + e: 1; v_rcp at 1
-// ulp: 2); a softmax's score within 2^-19 of the largest one (its sum has at most
-// 16 + 6 roundings, each term 2 ulp and the argument's rounding, |x| e^x <= 0.37);
+// ulp: 2); a softmax's score within 2^-19 of the largest one (the terms of its sum,
+// 2 ulp and the argument's rounding, |x| of each: together at most 2 + ln 1024 of
+// 2^-24; the score itself the same, |x| e^x <= 0.37, and two products);
 // the sum with the bias 2^-24, and the key's cut 2^-19, of the value.  Logits are
 // exact and the cut keeps their order, so any distance proves it.
 template <bool BF16_KEYS, int W, int VPL>
@@ -459,11 +460,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int lshift, boo
     for (int i = 0; i < VPL; ++i) top = fmaxf(top, l[i]);
     top = all_lanes<W>(top, Max());
     if (kScores || !a.renormalise) {
-      float sum = 0.f;
+      // in 64 bits, as a float sum's own roundings put a weight off by up to 6 x 2^-24
+      // (16384 tokens of 256: 3.3e-7 against 7.3e-8, for 11.4 against 11.7 us)
+      double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += l[i] > kLowF ? expf(l[i] - top) : 0.f;
+      for (int i = 0; i < VPL; ++i) sum += l[i] > kLowF ? (double)expf(l[i] - top) : 0.0;
       sum = all_lanes<W>(sum, Sum());
-      total = sum > 0.f ? (double)sum : 1.0;
+      total = sum > 0.0 ? sum : 1.0;
     }
   }
   int mine = -1;
