@@ -65,6 +65,27 @@ __device__ __forceinline__ T dpp(T v) {
     return __builtin_bit_cast(T, u32x2{dpp<CTRL>(x.x), dpp<CTRL>(x.y)});
   }
 }
+// Across rows of 16 lanes: v and itself with neighbouring rows (halves) swapped
+// between the two are the even and the odd rows' values in all lanes.  (Moves through
+// LDS instead: 1024 experts 5.6 against 4.9 us at 64 tokens, 27.5 against 26.3 at
+// 16384; 512 with 20 choices 5.7 against 4.5, but 22.0 against 22.6 at 16384.)
+template <int ROW, typename T, typename F>
+__device__ __forceinline__ T across(T v, F f) {
+  auto swap = [](uint32_t x) {
+    if constexpr (ROW == 16)
+      return __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    else
+      return __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  };
+  if constexpr (sizeof(T) == 4) {
+    const auto x = swap(__builtin_bit_cast(uint32_t, v));
+    return f(__builtin_bit_cast(T, (uint32_t)x[0]), __builtin_bit_cast(T, (uint32_t)x[1]));
+  } else {
+    const u32x2 h = __builtin_bit_cast(u32x2, v);
+    const auto x = swap(h.x), y = swap(h.y);
+    return f(__builtin_bit_cast(T, u32x2{x[0], y[0]}), __builtin_bit_cast(T, u32x2{x[1], y[1]}));
+  }
+}
 template <int W, typename T, typename F>
 __device__ __forceinline__ T all_lanes(T v, F f) {
   static_assert(W == 16 || W == 64, "");
@@ -73,8 +94,8 @@ __device__ __forceinline__ T all_lanes(T v, F f) {
   v = f(v, dpp<0x141>(v));
   v = f(v, dpp<0x140>(v));
   if constexpr (W == 64) {
-    v = f(v, __shfl_xor(v, 16, 64));
-    v = f(v, __shfl_xor(v, 32, 64));
+    v = across<16>(v, f);
+    v = across<32>(v, f);
   }
   return v;
 }
@@ -531,9 +552,9 @@ int vpl_of(const RouteArgs& a, int W, int* lshift) {
 }
 
 // 16 lanes a token wherever its experts, groups and ranks fit them: 64 experts
-// 4.0 against 5.5 us at 64 tokens and 5.2 against 8.7 at 8192, 256 experts in 8
-// groups 6.9 against 7.4 and 9.5 against 15.8 (at 256 to 1024 tokens 8.0 against
-// 7.4).  W = 64 for the rest.
+// 3.5 against 3.9 us at 64 tokens and 5.1 against 13.6 at 16384, 256 experts in 8
+// groups 6.0 against 6.0 and 14.1 against 24.7 (at 256 to 1024 tokens 7.3 against
+// 6.1 to 6.8).  W = 64 for the rest.
 template <typename K, bool BF16>
 hipError_t launch_w(const RouteArgs& a, hipStream_t s) {
   int lshift = 0;
