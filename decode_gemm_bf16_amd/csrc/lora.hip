@@ -212,16 +212,20 @@ __device__ __forceinline__ void stage_parts(const LoraSource& from, int len, int
 }
 
 // One workgroup: one tile; each of its 4 waves takes one group of 64 rows of B,
-// `reps` times over, and 16 NS tokens at a time.  v is the A operand (16 tokens x
+// `reps` times over, and 32 tokens at a time (64 at a time hold 84 registers instead
+// of 60, three workgroups a CU instead of four: 777 tokens on 4096 x 14336 18.4
+// against 15.7 us, 3999 on 4096 x 4096 33.1 against 29.1, 8192 on 14336 173 against 172;
+// 16 at a time 777 tokens of 128 ranks 54 against 37).  v is the A operand (16 tokens x
 // 16 ranks) and B the B operand; row 4 r + j of a group is column r of its j-th
 // 16-column product, so that a lane's results of the four products are 4
 // neighbouring columns of y, and a load or store of 16 bytes a lane covers 256
 // bytes of each of 4 tokens.  Row 4 q + k of the A operand is token q + 4 k of 16.
 // B lies in the order of the operands: a lane's 4 x 4 values of a group and rank
 // block are 32 bytes.
-template <int NS, bool STREAM, typename Args>
+template <bool STREAM, typename Args>
 __device__ __forceinline__ void expand_tile(const Args& a, const LoraProj& p, const PlanTile& tile,
                                             const LoraSource& from, int reps, LoraParts& parts) {
+  constexpr int NS = 2;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int groups = (p.rows + 63) / 64;
   const uint16_t* b = p.b + (int64_t)(tile.slot < 0 ? 0 : tile.slot) * p.rank16 * groups * 64 + lane * 16;
@@ -394,7 +398,7 @@ __device__ __forceinline__ void expand_few(const Args& a, const LoraProj& p, con
 // C: groups of 64 rows per wave; two at once where the tile has at most 4
 // tokens.  STREAM: y passes the caches by.
 template <int N, int C, bool STREAM>
-__global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraArgsOf<N> a) {
+__global__ __launch_bounds__(256, 4) void lora_expand_kernel(LoraArgsOf<N> a) {
   __shared__ __attribute__((aligned(16))) LoraParts parts;
   const LoraProj& p = a.proj[blockIdx.z];
   if (!plan_has(a, blockIdx.y)) return;
@@ -404,10 +408,8 @@ __global__ __launch_bounds__(256, C == 1 ? 3 : 4) void lora_expand_kernel(LoraAr
   const LoraSource from{p.part + (int64_t)tile.start * p.rank16, p.rank16, (int64_t)a.tokens * p.rank16, a.ksplit};
   if (tile.len <= 4)
     expand_few<kFew, STREAM, 4>(a, p, tile, from, C / kFew);
-  else if (C > 1 || tile.len <= 32)
-    expand_tile<2, STREAM>(a, p, tile, from, C, parts);
   else
-    expand_tile<4, STREAM>(a, p, tile, from, C, parts);
+    expand_tile<STREAM>(a, p, tile, from, C, parts);
 }
 
 // ---- both in one launch, for at most four tokens ----
@@ -477,9 +479,10 @@ hipError_t launch_apply(const LoraArgs& all, hipStream_t s) {
   hipLaunchKernelGGL(lora_shrink_kernel<N>, dim3(a.ksplit, a.halves ? 2 * a.tiles_max : a.tiles_max, rblocks * a.nproj),
                      dim3(64 * kShrinkWaves), 0, s, a);
   // Few tokens a slot: mostly tiles of a token or a few, whose workgroups take 1024
-  // columns (64 adapters of one token, gate and up of 14336 rows: 16.3 us against
-  // 30.2 with 256; 256 tokens of one adapter in 256 slots, which it does not suit,
-  // 20.5 against 14.7), if there are workgroups enough
+  // columns, if there are workgroups enough (gate and up of 14336 rows: 64 adapters of
+  // one token 16.3 us against 24.9 with 256, of four in a run 20.9 against 27.5, of
+  // four on average 27.8 against 29.2; 256 tokens of one adapter in 256 slots, which
+  // it does not suit, 30.6 against 16.0)
   if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
     launch_expand<N, 4>(a, rows, s);
   else
@@ -517,12 +520,12 @@ int64_t lora_tiles_max(int64_t tokens, int32_t slots) {
 }
 
 // Whether the shrink takes 32 tokens a workgroup: 136 tiles of 4096 columns 20 +
-// 174 us (shrink and expansion) against 19 + 191 with whole tiles in two parts.
+// 172 us (shrink and expansion) against 19 + 175 with whole tiles in two parts.
 bool lora_halves(int64_t tokens, int32_t slots, int nproj) { return lora_tiles_max(tokens, slots) * nproj >= 128; }
 
 // Parts of cols: up to two workgroups a CU, and two batches for each wave.  (More
 // parts cost the expansion, which reads all of them for every 256 columns of y:
-// 777 tokens on 4096 x 14336 in 4 parts 18.3 + 15.2 us, in 8 14.3 + 18.1.)
+// 777 tokens on 4096 x 14336 in 4 parts 19.0 + 14.5 us, in 8 15.3 + 15.7.)
 int lora_ksplit(int64_t tokens, int32_t slots, int64_t cols, int nproj) {
   const int64_t tiles = lora_tiles_max(tokens, slots) * nproj, batches = cols / 64;
   const int64_t blocks = lora_halves(tokens, slots, nproj) ? 2 * tiles : tiles;
