@@ -346,9 +346,12 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& at,
       const bool there = at.g < a.groups;
       const float in = all_lanes<W>(there && stays ? merit : -kLowF, Min());
       const float out = all_lanes<W>(there && !stays ? merit : kLowF, Max());
-      // the errors of up to two scores on each side, and the roundings of sums of this size
+      // The errors of up to two scores on each side, and the roundings of sums of this size.  Without
+      // a candidate in the groups left out there is nothing to decide, unless a sum may have passed
+      // float32's range: a merit of -inf is then that of a group with candidates (size is infinite).
       const float size = all_lanes<W>((hi > kLowF ? fabsf(hi) : 0.f) + (lo > kLowF ? fabsf(lo) : 0.f), Max());
-      if (out > kLowF && !(in - out > 4.f * eps + 0x1p-21f * size)) stays = stays_exact<W, VPL>(a, at, l, top);
+      if ((out > kLowF || size > __FLT_MAX__) && !(in - out > 4.f * eps + 0x1p-21f * size))
+        stays = stays_exact<W, VPL>(a, at, l, top);
     }
     if (!stays) {
 #pragma unroll

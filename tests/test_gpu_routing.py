@@ -195,6 +195,31 @@ def test_route_largest_values(env):
                 run_route(env, l, 3, dtype=dtype, score=score, bias=bias, renormalise=False)
 
 
+def test_route_merits_past_float32(env):
+    """Biases so large that a group's merit, a sum of two, has no place in float32: it
+    is compared in 64 bits, also against a group without candidates, which is behind."""
+    l = np.zeros((3, 8))
+    l[1, :4] = -INF  # group 0 has no candidates
+    l[2, 4:7] = -INF  # group 1 a single one: its merit is no sum
+    for bias, want in (((-3e38, -2e38), ([4, 5], [4, 5], [7, -1])), ((-2e38, -3e38), ([0, 1], [4, 5], [7, -1])),
+                       ((3e38, 2e38), ([0, 1], [4, 5], [0, 1]))):
+        for score in (0, 1):
+            e, _ = run_route(env, l, 2, score=score, bias=np.repeat(bias, 4), groups=2, group_score=1)
+            assert e.tolist() == list(want)
+    rng = np.random.default_rng(14)
+    for experts, groups, top_groups, top_k in ((8, 2, 1, 2), (60, 4, 2, 5), (256, 8, 3, 8), (512, 16, 5, 16), (990, 33, 5, 12)):
+        per = experts // groups
+        for size in (2e38, 3.4e38):
+            level = rng.choice([-size, -0.9 * size, -0.5 * size, 0.0, size], size=groups)
+            bias = np.repeat(level, per) * (1 - rng.integers(0, 3, size=experts) / 64)
+            logits = rng.normal(size=(60, experts))
+            logits[rng.random((60, groups)).repeat(per, axis=1) < 0.3] = -INF
+            for score in (0, 1):
+                for pairs in (0, 1):
+                    run_route(env, logits, top_k, score=score, bias=bias, groups=groups, top_groups=top_groups,
+                              group_score=pairs, renormalise=False)
+
+
 def test_route_strides_and_alignment(env):
     torch, uw = env
     rng = np.random.default_rng(13)
