@@ -375,6 +375,9 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
   if (work_bytes < need)
     return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, %lld tokens need %zu", work_bytes, (long long)tokens, need);
   const PlanParts parts = plan_parts(tokens, slots);
+  // the products with A go to the workspace while other workgroups read x and the plan
+  if (overlap(work_dev, need, x_dev, span(tokens, cols, ldx, 2)) || overlap(work_dev, need, plan_dev, parts.total))
+    return fail(UW_ERR_INVALID_ARG, "the workspace overlaps x or the plan");
   const uint8_t* m = static_cast<const uint8_t*>(plan_dev);
   uw::LoraArgs a{};
   int64_t written = 0;
@@ -389,6 +392,8 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
       return fail(UW_ERR_SHAPE, "row strides of projection %d must be >= rows and multiples of 4", i);
     if (!aligned(ys_dev[i], 16) || (base && !aligned(base, 16)))
       return fail(UW_ERR_INVALID_ARG, "bases and outputs must be 16-byte aligned");
+    if (base && overlap(work_dev, need, base, span(tokens, h->rows, lb, 4)))
+      return fail(UW_ERR_INVALID_ARG, "the workspace overlaps base %d", i);
     const size_t out = span(tokens, h->rows, ldy[i], 4);
     const bool in_place = base == ys_dev[i] && lb == ldy[i];
     bool bad = overlap(x_dev, span(tokens, cols, ldx, 2), ys_dev[i], out) ||

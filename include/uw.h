@@ -460,9 +460,9 @@ uw_status uw_lora_plan(const int32_t* slot_dev, int64_t tokens, int32_t slots, v
  * with row strides ldbase; ys_dev: n float outputs with row strides ldy (>=
  * rows, multiples of 4); all 16-byte aligned.  base_i may be y_i with the same
  * stride (in place: uw_matmul's output).  Tokens without an adapter get their
- * base.  work_dev: 256-byte aligned, at least uw_lora_workspace_bytes bytes;
- * calls that overlap in time must not share it.  UW_ERR_INVALID_ARG if the
- * current device is not the adapters'. */
+ * base.  work_dev: 256-byte aligned, at least uw_lora_workspace_bytes bytes,
+ * apart from every other buffer of the call; calls that overlap in time must not
+ * share it.  UW_ERR_INVALID_ARG if the current device is not the adapters'. */
 size_t uw_lora_workspace_bytes(const uw_lora* adapters, int32_t n, int64_t tokens);
 uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev, size_t plan_bytes,
                         const uint16_t* x_dev, int64_t ldx, const float* const* bases_dev, const int64_t* ldbase,

@@ -104,6 +104,43 @@ def test_lora_refuses_without_a_device_handle():
     assert L.uw_lora_apply(none, 1, A, 1 << 20, B, 64, one, None, one, ld, 4, D, 1 << 20, None) == uw.ERR_INVALID_ARG
 
 
+class AdaptersRecord(C.Structure):
+    """The host side of a uw_lora, as routing.cpp lays it out: without a device no call makes one."""
+    _fields_ = ([(k, C.c_int64) for k in ("rows", "cols", "rows64")] +
+                [(k, C.c_int32) for k in ("slots", "max_rank", "rank16", "device")] +
+                [(k, C.c_void_p) for k in ("mem", "a", "b", "table")])
+
+
+def test_lora_apply_refuses_overlaps():
+    """Each buffer that the call writes, against each other buffer of the call."""
+    tokens, rows, cols, slots = 100, 64, 128, 4
+    records = [AdaptersRecord(rows, cols, rows, slots, 16, 16, 0, None, None, None, None) for _ in range(2)]
+    hs = (C.c_void_p * 2)(*[C.addressof(r) for r in records])
+    plan_bytes = uw.lora_plan_bytes(tokens, slots)
+    need = L.uw_lora_workspace_bytes(hs, 2, tokens)
+    assert need > 0
+    xbytes, ybytes = tokens * cols * 2, tokens * rows * 4
+    plan, x, work, y0, y1, b0, b1 = (i << 28 for i in range(1, 8))
+
+    def call(plan=plan, x=x, work=work, ys=(y0, y1), bases=(b0, b1)):
+        ld = (C.c_int64 * 2)(rows, rows)
+        return L.uw_lora_apply(hs, 2, plan, plan_bytes, x, cols, (C.c_void_p * 2)(*bases), ld, (C.c_void_p * 2)(*ys), ld,
+                               tokens, work, need, None)
+
+    down, up = (lambda n: n - n % 256), (lambda n: n + -n % 256)
+    for kw in (dict(work=plan), dict(work=plan + down(plan_bytes - 1)), dict(work=plan - down(need - 1)),
+               dict(work=x), dict(work=x + down(xbytes - 1)), dict(work=x - down(need - 1)),
+               dict(work=b0), dict(work=b0 + down(ybytes - 1)), dict(work=b1 - down(need - 1)),
+               dict(work=y0), dict(work=y1 + down(ybytes - 1)), dict(ys=(y0, y0 + 16)), dict(ys=(x, y1)),
+               dict(ys=(y0, plan + 16)), dict(ys=(b1, y1)), dict(ys=(y0, b1 + 16))):
+        assert call(**kw) == uw.ERR_INVALID_ARG, kw
+        assert "overlap" in uw.last_error(), kw
+    if not torch.cuda.is_available():  # side by side, and in place, they go on to ask for the device
+        for kw in (dict(), dict(work=plan + up(plan_bytes)), dict(work=x - up(need)), dict(work=b1 + up(ybytes)),
+                   dict(bases=(y0, y1)), dict(bases=(None, b1))):
+            assert call(**kw) == uw.ERR_HIP, kw
+
+
 def test_moe_forward_refuses():
     assert uw.moe_workspace_bytes(0, 64, 64, 8, 2) == uw.moe_workspace_bytes(4, 64, 64, 8, 9) == 0
     assert uw.moe_workspace_bytes(4, 64, 64, 1025, 2) == 0
