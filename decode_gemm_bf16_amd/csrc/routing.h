@@ -61,6 +61,8 @@ constexpr int kLoraMaxProj = 4;
 struct LoraSlot {
   int32_t rank;
   float scale;
+  int32_t special;  // not 0: B holds infinities or NaN, or has held some since the slot was last empty
+  int32_t unused;
 };
 // One projection's adapters, both matrices in the order of the matrix
 // operands.  Slot i's A is a + i * rank16 * cols, [rank16 / 16][cols / 32][4][16][8]

@@ -424,9 +424,13 @@ uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, con
  * cols] and B [rows, rank], bf16, and a factor.  uw_lora_plan sorts a batch's
  * tokens by slot once; uw_lora_apply then adds, for any projection of any
  * layer, y[t] = base[t] + scale_i * B_i (A_i x[t]) for the token's slot i, on
- * top of uw_matmul's output.  Products accumulate in float32 and A_i x[t] is
- * never rounded below it.  The calls run on `stream` and except create and
- * free only launch kernels, so they can be captured.  1 <= tokens <= 2^20. */
+ * top of uw_matmul's output.  Products accumulate in float32 and scale_i * A_i
+ * x[t] is never rounded below it, except that its bits below 2^-133 (bfloat16's
+ * smallest step) are dropped.  Infinities and NaN in x, A, B and base reach the
+ * outputs that use them and no others, and give what the formula gives (an
+ * infinity in B times a value between 0 and 2^-110 may give NaN).  The calls run
+ * on `stream` and except create and free only launch kernels, so they can be
+ * captured.  1 <= tokens <= 2^20. */
 typedef struct uw_adapters* uw_lora;
 #define UW_LORA_MAX_RANK 256
 

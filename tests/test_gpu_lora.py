@@ -374,6 +374,64 @@ def test_infinities_stay_with_their_token(env):
     check(got[rest], xv[rest], index[rest], s.values, base[rest])
 
 
+@pytest.mark.parametrize("tokens,slots,rows,cols,max_rank", [
+    (3, 2, (528, 1040), 64, 5),     # one launch
+    (20, 1, (80,), 128, 3),
+    (70, 2, (48, 272, 16), 64, 70),  # two stagings of the products with A
+    (60, 40, (12336,), 64, 20),     # 1024 columns a workgroup, most tiles of one token
+])
+def test_infinities_in_b(env, tokens, slots, rows, cols, max_rank):
+    """Infinities and NaN in B give what the formula gives: also where a product with A
+    has few bits (here all are small whole numbers, zero among them) or is infinite itself."""
+    torch, uw = env
+    rng = np.random.default_rng(30 + tokens)
+    setups = []
+    for n in rows:
+        s = Setup(env, rng, slots, n, cols, max_rank, [0] * slots)
+        for i in range(slots):
+            r = max(1, max_rank - i)
+            a = rng.integers(-1, 2, size=(r, cols)).astype(np.float32) * (rng.random((r, cols)) < 0.1)
+            a[:, 5] = 1.0
+            b = values(rng, n, r)[1].astype(np.float32)
+            b[:8] = np.abs(b[:8])
+            if i != 1:  # slot 1's B is finite
+                b[rng.random(b.shape) < 0.3 / r] = INF
+                b[8:][rng.random(b[8:].shape) < 0.2 / r] = -INF
+                b[rng.random(b.shape) < 0.05 / r] = NAN
+            s.h.load(i, *(torch.from_numpy(v).to(torch.bfloat16).cuda() for v in (a, b)), 0.5)
+            s.values[i] = (a.astype(np.float64), b.astype(np.float64), 0.5)
+        setups.append(s)
+    xv = rng.integers(-3, 4, size=(tokens, cols)).astype(np.float64)
+    if tokens > 3:
+        xv[tokens // 2, 5] = INF
+    x = synth.f32_to_bf16_bits(xv.astype(np.float32))
+    index = np.arange(tokens) % (slots + 1)
+    bases = [rng.standard_normal((tokens, n), dtype=np.float32) for n in rows]
+
+    def compare():
+        for s, base, got in zip(setups, bases, apply(env, setups, x, index, bases)):
+            with np.errstate(invalid="ignore"):
+                want = routing.lora(xv, index, s.values, base)
+                plain = {i: (a, np.where(np.isfinite(b), b, 0.0), c) for i, (a, b, c) in s.values.items()}
+                bound = routing.lora_error_bound(xv, index, plain, base)
+            finite = np.isfinite(want)
+            assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got == INF, want == INF)
+            assert np.array_equal(got == -INF, want == -INF)
+            assert (np.abs(got[finite] - want[finite]) <= bound[finite]).all()
+
+    compare()
+    # finite again: over what was there, and in an emptied slot
+    for s in setups:
+        for i in range(slots):
+            a, b, _ = s.values[i]
+            b = np.where(np.isfinite(b), b, 1.0)
+            if i % 2:
+                s.h.clear(i)
+            s.h.load(i, *(torch.from_numpy(v).to(torch.bfloat16).cuda() for v in (a, b)), -1.5)
+            s.values[i] = (a, b, -1.5)
+    compare()
+
+
 def test_refusals(env):
     torch, uw = env
     rng = np.random.default_rng(14)
