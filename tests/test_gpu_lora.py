@@ -166,6 +166,83 @@ def test_long_columns(env, tokens, rows, cols, max_rank, slots):
     check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4])
+@pytest.mark.parametrize("projections", [2, 3, 4])
+def test_one_launch_of_several_projections(env, tokens, projections):
+    """Few tokens on projections of other rows (within one workgroup's 512, past it, an
+    end inside a wave's 64) and other ranks; some tokens share a slot."""
+    rng = np.random.default_rng(40 + tokens + 10 * projections)
+    slots, cols = 3, 320
+    shapes = ((208, 16), (1040, 64), (16, 3), (528, 33))[:projections]
+    setups = [Setup(env, rng, slots, n, cols, m, [m, max(1, m // 2), 0]) for n, m in shapes]
+    x, xv = values(rng, tokens, cols)
+    for index in (rng.integers(-1, slots, size=tokens), np.full(tokens, 1), np.full(tokens, 2)):
+        bases = [rng.standard_normal((tokens, n), dtype=np.float32) for n, _ in shapes]
+        for s, base, got in zip(setups, bases, apply(env, setups, x, index, bases)):
+            check(got, xv, index, s.values, base)
+
+
+@pytest.mark.parametrize("max_rank", [17, 64, 130])
+@pytest.mark.parametrize("tokens,slots,cols,shapes", [
+    (2000, 100, 192, (32,)),
+    (1000, 112, 2048, (16,)),       # and two parts of the columns
+    (700, 60, 192, (48, 16, 80)),
+])
+def test_half_tiles(env, max_rank, tokens, slots, cols, shapes):
+    """So many tiles that the product with A takes 32 tokens a workgroup: tiles of one
+    token to 64, ranks of one block of 16 to three of 64."""
+    rng = np.random.default_rng(tokens + max_rank)
+    ranks = np.zeros(slots, dtype=int)
+    used = rng.permutation(slots)[:9]
+    ranks[used] = [max_rank, max_rank, max_rank - 1, (max_rank + 1) // 2, 1, 16, 17, max_rank, max_rank - 13 if max_rank > 17 else 5]
+    setups = [Setup(env, rng, slots, n, cols, max_rank, ranks) for n in shapes]
+    index = np.concatenate([np.repeat(used[:6], [1, 31, 32, 33, 63, 64]), rng.choice(used, size=tokens - 274),
+                            rng.integers(-1, slots, size=50)])
+    rng.shuffle(index)
+    x, xv = values(rng, tokens, cols)
+    bases = [rng.standard_normal((tokens, n), dtype=np.float32) for n in shapes]
+    for s, base, got in zip(setups, bases, apply(env, setups, x, index, bases)):
+        check(got, xv, index, s.values, base)
+
+
+@pytest.mark.parametrize("max_rank", [64, 70])
+@pytest.mark.parametrize("slots", [3, 600])  # 256 columns a workgroup, and 1024
+def test_ranks_of_an_output_larger_than_the_caches(env, max_rank, slots):
+    rng = np.random.default_rng(max_rank + slots)
+    tokens, rows, cols = 2100, 16384, 64
+    ranks = np.zeros(slots, dtype=int)
+    used = rng.permutation(slots)[:8]
+    ranks[used] = [max_rank, max_rank - 3, 17, 64, 5, max_rank, 48, 1][:len(used)]
+    s = Setup(env, rng, slots, rows, cols, max_rank, ranks)
+    # a few tokens with adapters, in tiles of 1, 3, 4, 5 tokens and more; the others keep their base
+    index = np.full(tokens, -1)
+    index[:160] = np.concatenate([np.repeat(used[:3], [70, 33, 4]), rng.choice(used, size=53)])
+    if slots > 8:
+        index[:160] = np.concatenate([np.repeat(used, [1, 3, 4, 5, 40, 64, 33, 2]), rng.choice(used, size=8)])
+    order = rng.permutation(tokens)
+    index = index[order]
+    x, xv = values(rng, tokens, cols)
+    base = rng.standard_normal((tokens, rows), dtype=np.float32)
+    check(apply(env, [s], x, index, [base])[0], xv, index, s.values, base)
+
+
+@pytest.mark.parametrize("shapes", [((8208, 16), (2064, 130)), ((8208, 130), (272, 20)), ((4112, 70), (8208, 64), (1040, 5))])
+def test_wide_outputs_of_several_projections(env, shapes):
+    """1024 columns a workgroup on projections of other rows and ranks, on tiles of up
+    to four tokens, up to 32 and more."""
+    rng = np.random.default_rng(sum(n + m for n, m in shapes))
+    tokens, slots, cols = 200, 50, 128
+    ranks = rng.integers(0, 131, size=slots)
+    ranks[:4] = 130
+    setups = [Setup(env, rng, slots, n, cols, m, np.minimum(ranks, m)) for n, m in shapes]
+    index = np.concatenate([np.repeat([0, 1, 2, 3], [64, 35, 7, 3]), rng.integers(-1, slots, size=91)])
+    rng.shuffle(index)
+    x, xv = values(rng, tokens, cols)
+    bases = [rng.standard_normal((tokens, n), dtype=np.float32) for n, _ in shapes]
+    for s, base, got in zip(setups, bases, apply(env, setups, x, index, bases)):
+        check(got, xv, index, s.values, base)
+
+
 def test_small_magnitudes(env):
     """Products with A near 2^-110, whose lower parts bf16 holds as denormals."""
     rng = np.random.default_rng(22)
