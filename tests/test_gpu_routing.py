@@ -195,6 +195,45 @@ def test_route_largest_values(env):
                 run_route(env, l, 3, dtype=dtype, score=score, bias=bias, renormalise=False)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("experts,top_k,with_bias", [(8, 2, False), (60, 4, True), (256, 8, False), (256, 8, True),
+                                                      (1000, 5, True), (1024, 16, False)])
+def test_route_weights(env, experts, top_k, with_bias, dtype):
+    """How exact a weight is.  It is evaluated in 64 bits and rounded once, by 2^-24 of
+    itself; the terms of a softmax's sum alone are exponentials in float32, added in 64
+    bits: each is off by 2 ulp (2^-22) and by the rounding of its argument d (|d| 2^-24),
+    and the largest, exp(0), by nothing.  So the sum is off by at most the mean of 4 + |d|
+    over the other terms, each by its share, times 2^-24: nearly nothing where one
+    logit stands out (a float32 sum of such rows of 256 is off by up to 8 x 2^-24)."""
+    torch, uw = env
+    rng = np.random.default_rng(experts + top_k)
+    l = rng.normal(size=(300, experts)) * 1.5
+    l[:60] = -17.5 + rng.normal(size=(60, experts)) * 0.1  # about 2^-25 each
+    l[np.arange(60), np.arange(60) * 7 % experts] = rng.integers(0, 2, size=60)
+    l[60:80] *= 8
+    bias = rng.normal(size=experts).astype(np.float32) * np.float32(0.1) if with_bias else None
+    logits = torch.from_numpy(l.astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    seen = logits.double().cpu().numpy()
+    p = np.exp(seen - seen.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    d = seen.max(axis=1, keepdims=True) - seen
+    sums = (p * np.where(d > 0, 4 + d, 0.0)).sum(axis=1)[:, None]
+    assert sums[:60].max() < 0.02 * experts / 1024 + 0.01
+    for score in (0, 1):
+        for renormalise in (False, True):
+            e = torch.empty((300, top_k), dtype=torch.int32, device="cuda")
+            w = torch.empty((300, top_k), device="cuda")
+            print(f"weights 300x{experts} k={top_k} {dtype} score={score} renormalise={renormalise}", flush=True)
+            uw.route(logits, e, w, score=score, bias=None if bias is None else torch.from_numpy(bias).cuda(),
+                     renormalise=renormalise, scale=2.0)
+            torch.cuda.synchronize()
+            want_e, want = routing.route(seen, top_k, score, bias, renormalise=renormalise, scale=2.0)
+            assert np.array_equal(e.cpu().numpy(), want_e)
+            # (the oracle's own 64-bit roundings: 1200 of 2^-53 for the longest sum)
+            tol = 1 + 2.0 ** -18 + (sums if score == 0 and not renormalise else 0.0)
+            assert (np.abs(w.cpu().numpy() - want) <= tol * 2.0 ** -24 * want + 2.0 ** -150).all()
+
+
 def test_route_merits_past_float32(env):
     """Biases so large that a group's merit, a sum of two, has no place in float32: it
     is compared in 64 bits, also against a group without candidates, which is behind."""
