@@ -54,8 +54,10 @@ union ShrinkLds {
 // the wave's part of LDS 128 bytes of a row at a time and is read from there in
 // that order: loads of 64 bytes of 16 rows, as the operands have it, waste most
 // of a memory page's activation.  The waves' sums are added in LDS.
-// Bound by what a CU takes in at memory latency, about 22 GB/s each, so the work
-// is spread over all of them before anything else.
+// A wave waits for a batch's loads before its products and has nothing in flight
+// during them, so a CU takes in about 22 GB/s: one batch's bytes per memory latency.
+// That bounds it, and the work is spread over all CUs before anything else.  (128
+// registers, two of them spilled: 12 bytes of scratch a lane.)
 template <int NS, int NR, typename Args>
 __device__ __forceinline__ void shrink_tile(const Args& a, const LoraProj& p, const PlanTile& tile, int kpart,
                                             int ksplit, int rblock, int nr, ShrinkLds& lds, float* out, int64_t ldout) {
@@ -234,8 +236,8 @@ __device__ __forceinline__ void stage_parts(const LoraSource& from, int len, con
 }
 
 // One workgroup: one tile; each of its 4 waves takes one group of 64 rows of B,
-// `reps` times over, and 32 tokens at a time (64 at a time hold 84 registers instead
-// of 60, three workgroups a CU instead of four: 777 tokens on 4096 x 14336 18.4
+// `reps` times over, and 32 tokens at a time (64 at a time hold 164 registers instead
+// of 120, three waves a SIMD instead of four: 777 tokens on 4096 x 14336 18.4
 // against 15.7 us, 3999 on 4096 x 4096 33.1 against 29.1, 8192 on 14336 173 against 172;
 // 16 at a time 777 tokens of 128 ranks 54 against 37).  v is the A operand (16 tokens x
 // 16 ranks) and B the B operand; row 4 r + j of a group is column r of its j-th
@@ -507,8 +509,9 @@ hipError_t launch_apply(const LoraArgs& all, hipStream_t s) {
   // Few tokens a slot: mostly tiles of a token or a few, whose workgroups take 1024
   // columns, if there are workgroups enough (gate and up of 14336 rows: 64 adapters of
   // one token 16.3 us against 24.9 with 256, of four in a run 20.9 against 27.5, of
-  // four on average 27.8 against 29.2; 256 tokens of one adapter in 256 slots, which
-  // it does not suit, 30.6 against 16.0)
+  // four on average 27.8 against 29.2).  The number of slots stands in for the number
+  // of adapters in the batch, which is known on the device only: 256 tokens of one
+  // adapter in 256 slots take 30.6 against 16.0.
   if (a.tokens <= 4 * a.slots && (int64_t)a.tiles_max * rows * a.nproj >= 256 * 2048)
     launch_expand<N, 4>(a, rows, s);
   else
@@ -552,6 +555,12 @@ int64_t lora_tiles_max(int64_t tokens, int32_t slots) {
   const int64_t t = (tokens + kPlanTile - 1) / kPlanTile + slots;  // each label's last tile may be short
   return t < tokens ? t : tokens;
 }
+
+// These rules see how many tiles a batch of this size can have at most, with every
+// slot of the handle in use, and not how many it has: the host does not know the plan.
+// A batch of few adapters in a handle of many slots runs with fewer workgroups than
+// would suit it (plan and call, 512 tokens of one adapter of 16 ranks on 4096 x
+// 14336: 23.5 us in 4 slots, 44 in 128 or 512).
 
 // Whether the shrink takes 32 tokens a workgroup: 136 tiles of 4096 columns 20 +
 // 172 us (shrink and expansion) against 19 + 175 with whole tiles in two parts.

@@ -484,8 +484,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int lshift, boo
     for (int i = 0; i < VPL; ++i) top = fmaxf(top, l[i]);
     top = all_lanes<W>(top, Max());
     if (kScores || !a.renormalise) {
-      // in 64 bits, as a float sum's own roundings put a weight off by up to 6 x 2^-24
-      // (16384 tokens of 256: 3.3e-7 against 7.3e-8, for 11.4 against 11.7 us)
+      // Added in 64 bits, as a float sum's own roundings put a weight off by up to 6 x
+      // 2^-24 (16384 tokens of 256: 3.3e-7 against 7.3e-8, for 11.4 against 11.7 us).  Its
+      // terms stay float32: they are off by 2 ulp and |l - top| 2^-24 at most, which nearly
+      // cancels in the sum; exponentials in 64 bits make 7.3e-8 the 6.0e-8 of the result's
+      // own rounding, for 15.5 against 12.1 us (16384 tokens of 1024: 44.7 against 34.6).
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) sum += l[i] > kLowF ? (double)expf(l[i] - top) : 0.0;
@@ -554,10 +557,13 @@ int vpl_of(const RouteArgs& a, int W, int* lshift) {
   return per % 4 == 0 && per > 3 * L ? (per / 4 + L - 1) / L * 4 : (per + L - 1) / L;
 }
 
-// 16 lanes a token wherever its experts, groups and ranks fit them: 64 experts
-// 3.5 against 3.9 us at 64 tokens and 5.1 against 13.6 at 16384, 256 experts in 8
-// groups 6.0 against 6.0 and 14.1 against 24.7 (at 256 to 1024 tokens 7.3 against
-// 6.1 to 6.8).  W = 64 for the rest.
+// 16 lanes a token wherever its experts, groups and ranks fit them, whatever the
+// number of tokens: 64 experts 3.5 against 3.9 us at 64 tokens and 5.1 against 13.6
+// at 16384; 256 experts in 8 groups 14 to 16 against 24 to 25 at 16384.  Where few
+// waves are at work those 256 take more in 16 lanes (16 values a lane instead of 4):
+// 6.5 against 5.9 us at one token, 6.8 against 6.5 to 6.8 at 64, 6.9 to 8 against 6.7
+// at 512, 7.4 to 8.5 against 7.2 to 8.6 at 1024, which no rule is made for.  W = 64
+// for the rest.
 template <typename K, bool BF16>
 hipError_t launch_w(const RouteArgs& a, hipStream_t s) {
   int lshift = 0;

@@ -1451,7 +1451,8 @@ uw_status moe_impl(const uw_handle* handles, const int32_t* pipelines, const voi
     return st;
   std::vector<int32_t> host(ne + 1);
   UW_HIP(hipMemcpyAsync(host.data(), offsets, size_t(ne + 1) * 4, hipMemcpyDeviceToHost, main));
-  // the copy of the activations needs no host: it runs while the host waits
+  // The sizes go to pageable memory, a copy that may return only when the stream is through
+  // with it; the dispatch queued behind it is waited for as well.
   st = uw_dispatch_rows(x, hidden, slot, tokens, c->top_k, hidden, xs, n, main);
   UW_HIP(hipStreamSynchronize(main));  // also on failure: the copy writes `host`
   if (st != UW_OK) return st;
