@@ -31,7 +31,8 @@ EXPORTED = [
     "uw_mlp_forward", "uw_mlp_workspace_bytes", "uw_mlp_forward_noalloc", "uw_stack_forward", "uw_stack_workspace_bytes",
     "uw_route", "uw_group_rows_workspace_bytes", "uw_group_rows", "uw_dispatch_rows", "uw_combine_rows",
     "uw_moe_workspace_bytes", "uw_moe_forward", "uw_lora_create", "uw_lora_load", "uw_lora_free", "uw_lora_plan_bytes",
-    "uw_lora_plan", "uw_lora_workspace_bytes", "uw_lora_apply", "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
+    "uw_lora_plan", "uw_lora_workspace_bytes", "uw_lora_apply", "uw_cache_write", "uw_attend_workspace_bytes", "uw_attend",
+    "uw_cache_copy_pages", "uw_cache_keep", "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
 ]
 
 F32, BF16 = 0, 1
@@ -62,6 +63,19 @@ class RouteConfig(C.Structure):
         ("experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("groups", C.c_int32),
         ("top_groups", C.c_int32), ("group_score", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float),
     ]
+
+
+class CacheConfig(C.Structure):
+    _fields_ = [("heads", C.c_int32), ("kv_heads", C.c_int32), ("dim", C.c_int32), ("page", C.c_int32),
+                ("pages", C.c_int64)]
+
+
+class Rotary(C.Structure):
+    _fields_ = [("axes", C.c_int32), ("pairs", C.c_int32), ("adjacent", C.c_int32)]
+
+
+class AttendConfig(C.Structure):
+    _fields_ = [("scale", C.c_float), ("cap", C.c_float), ("window", C.c_int32)]
 
 
 def _preload_runtime() -> None:
@@ -128,6 +142,13 @@ def _load() -> C.CDLL:
         "uw_lora_workspace_bytes": ([C.POINTER(vp), i32, i64], C.c_size_t),
         # (its five arrays are passed by address: one block of memory holds them)
         "uw_lora_apply": ([vp, i32, vp, C.c_size_t, vp, i64, vp, vp, vp, vp, i64, vp, C.c_size_t, vp], st),
+        "uw_cache_write": ([C.POINTER(CacheConfig), C.POINTER(Rotary), vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp, i64,
+                            vp, i64, vp, vp, vp], st),
+        "uw_attend_workspace_bytes": ([i64, i64, i32, i32, i32, i64, i64], C.c_size_t),
+        "uw_attend": ([C.POINTER(CacheConfig), C.POINTER(AttendConfig), vp, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp,
+                       vp, vp, i32, i64, i64, i64, i64, vp, i64, i32, vp, vp, C.c_size_t, vp], st),
+        "uw_cache_copy_pages": ([C.POINTER(CacheConfig), i64, vp, vp, vp, vp, i64, vp], st),
+        "uw_cache_keep": ([C.POINTER(CacheConfig), i64, vp, vp, vp, i64, i64, vp, vp, i32, i64, vp, vp], st),
         "uw_stream_create": ([i32, i32, C.POINTER(vp)], st),
         "uw_stream_destroy": ([vp], st),
         "uw_device_cu_count": ([], i32),
@@ -392,16 +413,16 @@ def grouped_matmul(experts, x, y, row_offsets, pipeline: int = P_AUTO) -> None:
 # strides and device.  A decode step calls them hundreds of times, on kernels
 # of a few microseconds, so a check costs one attribute of the tensor each.
 
-_torch = _Tensor = _f32 = _bf16 = _i32 = _either = None
+_torch = _Tensor = _f32 = _bf16 = _i32 = _i64 = _either = None
 
 
 def _device() -> int:
     """The current GPU's index (-2 without one: no tensor's device has that index)."""
-    global _torch, _Tensor, _f32, _bf16, _i32, _either
+    global _torch, _Tensor, _f32, _bf16, _i32, _i64, _either
     if _torch is None:
         import torch
         _Tensor, _torch = torch.Tensor, torch
-        _f32, _bf16, _i32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+        _f32, _bf16, _i32, _i64 = (torch.float32,), (torch.bfloat16,), (torch.int32,), (torch.int64,)
         _either = _f32 + _bf16
     try:
         return _torch.cuda.current_device()
@@ -636,3 +657,134 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
     at, step = C.addressof(block), 8 * n
     _check(_lib.uw_lora_apply(at, n, pp, pb, xp, ldx, at + step, at + 2 * step, at + 3 * step, at + 4 * step, t, wp, wb,
                               _stream_ptr(stream)))
+
+
+# ---- a paged cache of keys and values, and attention over it ----
+#
+# A layer's cache is two bfloat16 tensors kc and vc [pages, kv_heads, page, dim], all
+# layers' [layers, pages, kv_heads, page, dim] (kc[l] is one layer's).  Within a page
+# of a head the elements are in the order of the matrix operands (include/uw.h).
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_config(heads, kv_heads, dim, page, pages) -> CacheConfig:
+    return CacheConfig(heads, kv_heads, dim, page, pages)
+
+
+@functools.lru_cache(maxsize=64)
+def _attend_config(scale, cap, window) -> AttendConfig:
+    return AttendConfig(scale, cap, window)
+
+
+@functools.lru_cache(maxsize=64)
+def _rotary(axes, pairs, adjacent) -> Rotary:
+    return Rotary(axes, pairs, int(bool(adjacent)))
+
+
+def _cache_shape(kc, dims: int):
+    if not isinstance(kc, _Tensor):
+        raise TypeError("kc must be a torch tensor")
+    s = kc.shape
+    if len(s) != dims:
+        raise ValueError(f"kc must have {dims} dimensions, not {len(s)}")
+    return s
+
+
+def _heads(cols: int, dim: int, name: str) -> int:
+    if dim < 1 or cols % dim:
+        raise ValueError(f"{name} must have a multiple of {dim} columns, not {cols}")
+    return cols // dim
+
+
+def cache_write(q, k, v, positions, freqs, slots, qr, kc, vc, axis=None, adjacent: bool = False, stream=None) -> None:
+    """Turn q and k by their rotary positions, write k and v to the cache (``uw_cache_write``):
+    q [tokens, heads * dim] (or None) -> qr, bfloat16; k, v [tokens, kv_heads * dim], all float32
+    or all bfloat16; positions [axes, tokens] and slots [tokens] int32, freqs [pairs] float32,
+    axis [pairs] int32 or None."""
+    dev = _device()
+    shape = pages, kv, page, dim = _cache_shape(kc, 4)
+    t = _shape2(k, "k")[0]
+    kind = (k.dtype,) if k.dtype in _either else _either
+    kp, ldk = _rows(k, "k", kind, (t, kv * dim), dev)
+    vp, ldv = _rows(v, "v", kind, (t, kv * dim), dev)
+    heads = qp = ldq = op = ldo = 0
+    if q is not None:
+        rows = _shape2(q, "q")
+        qp, ldq = _rows(q, "q", kind, (t, rows[1]), dev)
+        heads = _heads(rows[1], dim, "q")
+        op, ldo = _rows(qr, "qr", _bf16, (t, rows[1]), dev)
+    axes = _shape2(positions, "positions")[0]
+    pairs = freqs.numel()
+    _check(_lib.uw_cache_write(_cache_config(heads, kv, dim, page, pages), _rotary(axes, pairs, adjacent), qp, ldq, kp,
+                               ldk, vp, ldv, F32 if k.dtype == _f32[0] else BF16,
+                               _tensor(positions, "positions", _i32, (axes, t), dev),
+                               _tensor(freqs, "freqs", _f32, (pairs,), dev),
+                               None if axis is None else _tensor(axis, "axis", _i32, (pairs,), dev),
+                               _tensor(slots, "slots", _i32, (t,), dev), t, op, ldo,
+                               _tensor(kc, "kc", _bf16, shape, dev), _tensor(vc, "vc", _bf16, shape, dev),
+                               _stream_ptr(stream)))
+
+
+def attend_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int, max_tokens: int,
+                           max_length: int) -> int:
+    return _lib.uw_attend_workspace_bytes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length)
+
+
+def attend(q, kc, vc, offsets, lengths, tables, y, work=None, scale: float | None = None, cap: float = 0.0,
+           window: int = 0, slopes=None, prefix=None, first=None, mask=None, lse=None, max_tokens: int | None = None,
+           max_length: int | None = None, stream=None) -> None:
+    """Attention of each sequence's new tokens over its pages (``uw_attend``): q [tokens,
+    heads * dim] bfloat16 -> y bfloat16 or float32; offsets [seqs + 1], lengths [seqs] and tables
+    [seqs, max_pages] int32; slopes [heads] float32, prefix [seqs] and first [tokens] int32, mask
+    [tokens, words] int64, lse [tokens, heads] float32.  scale None: dim ** -0.5.  max_tokens and
+    max_length (None: all tokens, the tables' reach) say what to lay the call out for; work is
+    sized for the same numbers."""
+    dev = _device()
+    shape = pages, kv, page, dim = _cache_shape(kc, 4)
+    rows = t, cols = _shape2(q, "q")
+    heads = _heads(cols, dim, "q")
+    qp, ldq = _rows(q, "q", _bf16, rows, dev)
+    yp, ldy = _rows(y, "y", _either, rows, dev)
+    table = n, reach = _shape2(tables, "tables")
+    tp, ldt = _rows(tables, "tables", _i32, table, dev)
+    words = 0 if mask is None else _shape2(mask, "mask")[1]
+    wp, wb = _bytes(work, "work", dev)
+    _check(_lib.uw_attend(_cache_config(heads, kv, dim, page, pages),
+                          _attend_config(dim ** -0.5 if scale is None else scale, cap, window), qp, ldq,
+                          _tensor(kc, "kc", _bf16, shape, dev), _tensor(vc, "vc", _bf16, shape, dev),
+                          _tensor(offsets, "offsets", _i32, (n + 1,), dev),
+                          _tensor(lengths, "lengths", _i32, (n,), dev), tp, ldt, reach,
+                          None if slopes is None else _tensor(slopes, "slopes", _f32, (heads,), dev),
+                          None if prefix is None else _tensor(prefix, "prefix", _i32, (n,), dev),
+                          None if first is None else _tensor(first, "first", _i32, (t,), dev),
+                          None if mask is None else _tensor(mask, "mask", _i64, (t, words), dev), words, t, n,
+                          t if max_tokens is None else max_tokens, reach * page if max_length is None else max_length,
+                          yp, ldy, F32 if y.dtype == _f32[0] else BF16,
+                          None if lse is None else _tensor(lse, "lse", _f32, (t, heads), dev), wp, wb,
+                          _stream_ptr(stream)))
+
+
+def cache_copy_pages(kc, vc, src, dst, stream=None) -> None:
+    """Copy page src[i] to page dst[i] in all layers (``uw_cache_copy_pages``): kc, vc
+    [layers, pages, kv_heads, page, dim], src and dst [n] int32."""
+    dev = _device()
+    shape = layers, pages, kv, page, dim = _cache_shape(kc, 5)
+    n = src.numel()
+    _check(_lib.uw_cache_copy_pages(_cache_config(0, kv, dim, page, pages), layers, _tensor(kc, "kc", _bf16, shape, dev),
+                                    _tensor(vc, "vc", _bf16, shape, dev), _tensor(src, "src", _i32, (n,), dev),
+                                    _tensor(dst, "dst", _i32, (n,), dev), n, _stream_ptr(stream)))
+
+
+def cache_keep(kc, vc, tables, starts, kept, lengths, stream=None) -> None:
+    """Move the rows of accepted drafted tokens to their places in all layers (``uw_cache_keep``):
+    kc, vc [layers, pages, kv_heads, page, dim]; tables [seqs, max_pages], starts [seqs], kept
+    [seqs, most] int32; lengths [seqs] int32 is written."""
+    dev = _device()
+    shape = layers, pages, kv, page, dim = _cache_shape(kc, 5)
+    table = n, reach = _shape2(tables, "tables")
+    tp, ldt = _rows(tables, "tables", _i32, table, dev)
+    most = _shape2(kept, "kept")[1]
+    _check(_lib.uw_cache_keep(_cache_config(0, kv, dim, page, pages), layers, _tensor(kc, "kc", _bf16, shape, dev),
+                              _tensor(vc, "vc", _bf16, shape, dev), tp, ldt, reach,
+                              _tensor(starts, "starts", _i32, (n,), dev), _tensor(kept, "kept", _i32, (n, most), dev),
+                              most, n, _tensor(lengths, "lengths", _i32, (n,), dev), _stream_ptr(stream)))

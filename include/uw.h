@@ -473,6 +473,122 @@ uw_status uw_lora_apply(const uw_lora* adapters, int32_t n, const void* plan_dev
                         float* const* ys_dev, const int64_t* ldy, int64_t tokens, void* work_dev, size_t work_bytes,
                         void* stream);
 
+/* ---- A paged cache of keys and values, and attention over it ----
+ *
+ * What lies between the q, k and v projections of an attention layer and its
+ * output projection.  A layer's cache is two arrays of `pages` pages, k_cache and
+ * v_cache, bf16 [pages, kv_heads, page, dim]; a page holds `page` consecutive
+ * places of one sequence, and a sequence's table names its pages in order.  Place
+ * o of a page of one head is laid out in the order of the matrix operands:
+ * element d of the key at ((o / 32 * dim / 8 + d / 8) * 32 + o % 32) * 8 + d % 8,
+ * that of the value at
+ * ((o / 16 * 2 + o / 4 % 2) * dim + d) * 8 + o / 8 % 2 * 4 + o % 4 of the head's
+ * page * dim elements.  Memory that was never written may hold anything.
+ *
+ * These calls only launch kernels on `stream` (NULL = the null stream), allocate
+ * nothing and can be captured into a graph.  All pointers are device memory of the
+ * current device, the caches, rows and workspaces 16-byte aligned.  Outputs must
+ * not overlap inputs or each other.  Values in index arrays that name no page,
+ * place or token of the call are safe; what they mean is said with each call.
+ * 1 <= tokens <= 2^20, 1 <= seqs <= 65535, 1 <= layers <= 4096. */
+typedef struct {
+  int32_t heads;     /* query heads: a multiple of kv_heads, up to 64 times and 256  */
+  int32_t kv_heads;  /* heads of the cache: 1..128; query head h reads head
+                        h / (heads / kv_heads)                                       */
+  int32_t dim;       /* elements of a head: 64, 96, 128 or 256                       */
+  int32_t page;      /* places of a page: 32, 64, 128 or 256                         */
+  int64_t pages;     /* pages of a layer; pages * page < 2^31                        */
+} uw_cache_config;
+
+typedef struct {
+  int32_t axes;      /* 1..4, e.g. time, height and width                            */
+  int32_t pairs;     /* pairs of elements turned in each head: 0..dim / 2, the first
+                        2 * pairs elements; the others stay                          */
+  int32_t adjacent;  /* pair j is elements j and j + pairs, or 2j and 2j + 1 if
+                        nonzero                                                      */
+} uw_rotary;
+
+/* Turn q and k by their rotary positions and write k and v to the cache.  Pair
+ * (a, b) number j of a token becomes (a cos t - b sin t, a sin t + b cos t), t =
+ * positions[axis[j]][token] * freqs[j], formed in 64 bits and exact for far
+ * positions; results are rounded to bf16 once.  q_dev [tokens, heads * dim],
+ * k_dev and v_dev [tokens, kv_heads * dim] of `type` (UW_F32, e.g. uw_matmul's
+ * outputs, or UW_BF16), with row strides (multiples of 8); q may be NULL (keys and
+ * values alone).  positions_dev int32 [axes, tokens]; freqs_dev float [pairs];
+ * axis_dev int32 [pairs] or NULL (all 0), a pair with an axis outside 0..axes-1 is
+ * not turned.  slots_dev int32 [tokens]: page * config->page + place of the token's
+ * row; a token with any other number is not written (its q is).  No two tokens
+ * may name one slot.  q_out_dev bf16 [tokens, heads * dim], row stride ldq_out. */
+uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
+                         const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
+                         const int32_t* positions_dev, const float* freqs_dev, const int32_t* axis_dev,
+                         const int32_t* slots_dev, int64_t tokens, uint16_t* q_out_dev, int64_t ldq_out,
+                         uint16_t* k_cache_dev, uint16_t* v_cache_dev, void* stream);
+
+typedef struct {
+  float scale;     /* factor of q k: positive, finite                                */
+  float cap;       /* 0, or scores become cap * tanh(scale q k / cap)                */
+  int32_t window;  /* 0, or only keys less than so far behind are seen               */
+} uw_attend_config;
+
+/* Attention of each sequence's new tokens over its keys:
+ *   y = sum over seen keys of softmax(x) v,  x = scale q k, capped, - slope |distance|.
+ * Sequence b has tokens offsets[b] .. offsets[b+1]-1 of q and y, which are its last
+ * ones: its lengths[b] keys count them, at places 0 .. lengths[b]-1, place p in page
+ * tables[b][p / page] (max_pages entries a row, row stride ldt).  Token i of n sits
+ * at place lengths[b] - n + i.  It sees key k
+ *   - where k is not behind its own place, or, with prefix_dev (int32 [seqs]), k <
+ *     prefix[b];
+ *   - with mask_dev (uint64 [tokens, mask_words], a tree of drafted tokens): where k <
+ *     lengths[b] - n, or bit j = k - (lengths[b] - n) of its row is set (word j / 64,
+ *     bit j % 64; bits beyond the words are 0; its own bit is no exception);
+ *   - and, with first_dev (int32 [tokens]), k >= first[token] (a document's start);
+ *   - and, with a window, distance < window;
+ *   - and k's page is one of the cache's, and within max_pages.
+ * distance is the token's place less k; with a mask a drafted token stands, as query
+ * and as key, at lengths[b] - n + (set bits of its row) - 1.  slopes_dev: float
+ * [heads].  A token that sees no key gets y = 0 and lse -inf, as does one whose
+ * scores are all -inf.  Infinities and NaN of keys and values reach the tokens that
+ * see them and no others (an infinite value whose weight underflows gives NaN).
+ * q_dev bf16 [tokens, heads * dim], row stride ldq (a multiple of 8); y_dev of
+ * y_type (UW_BF16, or UW_F32), row stride ldy (a multiple of 8); lse_dev float
+ * [tokens, heads]: the logarithm of the sum of exp(x), or NULL.  Scores and sums are
+ * float32; the weights exp(x - max) are rounded to bf16 before the product with v.
+ * Tokens of q in no sequence leave their rows of y and lse as they are; offsets must
+ * not fall.
+ * max_tokens (1..tokens) and max_length (1..2^30) are the sizes the call is laid out
+ * for, the most tokens and keys of one sequence: any other lengths are right too, but
+ * slower.  work_dev: uw_attend_workspace_bytes bytes for the same numbers (may be NULL
+ * where that is 0; 0 for arguments out of range); it belongs to one call at a time. */
+size_t uw_attend_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                                 int64_t max_tokens, int64_t max_length);
+uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* options, const uint16_t* q_dev, int64_t ldq,
+                    const uint16_t* k_cache_dev, const uint16_t* v_cache_dev, const int32_t* offsets_dev,
+                    const int32_t* lengths_dev, const int32_t* tables_dev, int64_t ldt, int64_t max_pages,
+                    const float* slopes_dev, const int32_t* prefix_dev, const int32_t* first_dev,
+                    const uint64_t* mask_dev, int32_t mask_words, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                    int64_t max_length, void* y_dev, int64_t ldy, int32_t y_type, float* lse_dev, void* work_dev,
+                    size_t work_bytes, void* stream);
+
+/* Copy page src[i] to page dst[i], keys and values of all layers, i < n <= pages:
+ * k_cache_dev and v_cache_dev are [layers, pages, kv_heads, page, dim].  Pairs with
+ * a number outside the pages are skipped.  No page may be the destination of two
+ * pairs, nor of one and the source of another.  (config->heads is not read.) */
+uw_status uw_cache_copy_pages(const uw_cache_config* config, int64_t layers, uint16_t* k_cache_dev,
+                              uint16_t* v_cache_dev, const int32_t* src_dev, const int32_t* dst_dev, int64_t n,
+                              void* stream);
+
+/* Keep the accepted ones of each sequence's drafted tokens: kept_dev int32 [seqs,
+ * most] lists them, rising, up to the first entry that is negative or does not rise;
+ * the row at place starts[b] + kept[b][i] moves to place starts[b] + i, keys and
+ * values of all layers ([layers, pages, ...] as above), and lengths_dev[b] becomes
+ * starts[b] + the list's length.  Tables as in uw_attend; a row whose place has no
+ * page in the cache is not moved.  Sequences must not share the pages written.  1 <=
+ * most <= 256. */
+uw_status uw_cache_keep(const uw_cache_config* config, int64_t layers, uint16_t* k_cache_dev, uint16_t* v_cache_dev,
+                        const int32_t* tables_dev, int64_t ldt, int64_t max_pages, const int32_t* starts_dev,
+                        const int32_t* kept_dev, int32_t most, int64_t seqs, int32_t* lengths_dev, void* stream);
+
 /* ---- Streams with a CU mask (section 九's decode/compute split) ---- */
 
 /* Create a stream limited to compute units [cu_first, cu_first + cu_count)

@@ -37,7 +37,7 @@ from .gemm import (  # noqa: F401
     bf16_to_f64, f64_to_bf16_rne, matmul_fp64, matmul_fp64_rows, silu_mul_bf16,
     mlp_layer_fp64, rel_err,
 )
-from . import routing  # noqa: F401
+from . import attention, routing  # noqa: F401
 
 # Every oracle function and what pins it (tests/test_oracle_*.py).  None is
 # "parity unpinned".
@@ -57,6 +57,9 @@ PARITY = {
                                 "(an independent implementation of the same layout); header fields by struct",
     "routing.route": "hand-worked choices; weights against scipy's softmax and expit; group choices by brute force",
     "routing.group_rows/dispatch_rows/combine_rows": "hand-worked case; round trip through unit weights",
+    "attention.key_index/value_index": "one-to-one over a page; neighbours by hand",
+    "attention.turn/visible": "hand-worked cases, trees among them",
+    "attention.attend": "scipy's softmax and log_softmax; exact means of equal scores",
     "routing.lora": "exact rational sums; the merged weight W + scale B A",
     "transcode_bundle": "equals palette_encode of the original weights (the Huffman round trip is exact)",
 }
