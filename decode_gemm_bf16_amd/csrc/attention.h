@@ -75,14 +75,18 @@ struct AttendArgs {
   float scale, cap;
   bool y_bf16;
 };
+// Rows of a workgroup of the kernel for many rows.
+constexpr int kAttendRows = 128;
 // The rule on sizes that chooses kernel and parts.
 struct AttendPlan {
-  bool wide;  // 128 rows a workgroup, else 32
+  bool wide;  // kAttendRows a workgroup, else 32
   int32_t splits, chunk;
   size_t bytes;  // of the workspace
 };
 AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
                        int64_t max_length);
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t s);
+hipError_t launch_attend_few(const AttendArgs& a, hipStream_t s);   // (with its parts set)
+hipError_t launch_attend_many(const AttendArgs& a, hipStream_t s);
 
 }  // namespace uw
