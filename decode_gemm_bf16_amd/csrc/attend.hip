@@ -6,11 +6,26 @@ namespace {
 
 // ---- the parts of split keys, joined ----
 //
-// A workgroup joins 8 rows, or one row whose parts its 8 groups of 32 lanes divide
-// (ONE), 4 elements of 32 columns a lane.
+// A workgroup joins 8 rows, 32 lanes each, or one row whose parts its 8 groups of 32
+// lanes divide (ONE).  Up to 32 parts, and 256: a lane has each part's maximum and weight;
+// then 4 elements of 32 columns a lane, 4 parts' loads in flight.
+constexpr int kJoinAtOnce = 4;
+
+__device__ __forceinline__ float max32(float v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+__device__ __forceinline__ float sum32(float v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
 template <bool ONE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   __shared__ __attribute__((aligned(16))) float red[8][256];
+  __shared__ float factor[256], tops[8], weights[8];
   const int grp = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int64_t rows = (int64_t)a.tokens * a.heads;
   const int first = a.offsets[0], last = a.offsets[a.seqs];
@@ -19,55 +34,90 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     const int64_t row = ONE ? r0 : r0 * 8 + grp;
     const int t = (int)(row / a.heads), h = (int)(row - (int64_t)t * a.heads);
     const bool live = row < rows && t >= first && t < last;
-    float m = kNone, weight = 0.f;
-    f32x4 o[2] = {};
-    if (live) {
-      for (int z = 0; z < a.splits; ++z) m = __builtin_fmaxf(m, ml[((int64_t)z * rows + row) * 2]);
-      const float ref = m == kNone ? 0.f : m;
-      for (int z = 0; z < a.splits; ++z) {
-        const f32x2 e = *(const f32x2*)(ml + ((int64_t)z * rows + row) * 2);
-        if (e.y == 0.f) continue;
-        const float f = __builtin_amdgcn_exp2f(e.x - ref);
-        weight += e.y * f;
-        if (ONE && (z & 7) != grp) continue;
-        const float* p = a.part + ((int64_t)z * rows + row) * a.dim;
+    if (ONE && !live) continue;  // (the whole workgroup)
+    const int mine = ONE ? threadIdx.x : l;
+    f32x2 e = {kNone, 0.f};
+    if (live && mine < a.splits) e = *(const f32x2*)(ml + ((int64_t)mine * rows + row) * 2);
+    float m = max32(e.x), f = 0.f, weight;
+    if (ONE) {
+      if (l == 0) tops[grp] = m;
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int d = i * 128 + l * 4;
-          if (d < a.dim) o[i] += f * *(const f32x4*)(p + d);
+      for (int k = 0; k < 8; ++k) m = __builtin_fmaxf(m, tops[k]);
+    }
+    f = e.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(e.x - (m == kNone ? 0.f : m));
+    weight = sum32(e.y * f);
+    // a part without weight has written no sums
+    const bool there = e.y != 0.f;
+    if (ONE) {
+      factor[mine] = there ? f : -1.f;
+      if (l == 0) weights[grp] = weight;
+      __syncthreads();
+      weight = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) weight += weights[k];
+    }
+    f32x4 o[2] = {};
+    const float* const part = a.part + row * a.dim;
+    const int step = ONE ? 8 : 1;
+    if (live) {
+      for (int z0 = ONE ? grp : 0; z0 < a.splits; z0 += step * kJoinAtOnce) {
+        f32x4 v[kJoinAtOnce][2];
+        float g[kJoinAtOnce];
+#pragma unroll
+        for (int k = 0; k < kJoinAtOnce; ++k) {
+          const int z = z0 + k * step;
+          if (ONE)
+            g[k] = z < a.splits ? factor[z] : -1.f;
+          else
+            g[k] = __shfl(there ? f : -1.f, (threadIdx.x & 32) + (z < 32 ? z : 31), 64);
+          if (z >= a.splits) g[k] = -1.f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int d = i * 128 + l * 4;
+            v[k][i] = f32x4{};
+            if (d < a.dim && !(g[k] < 0.f)) v[k][i] = *(const f32x4*)(part + (int64_t)z * rows * a.dim + d);
+          }
         }
+#pragma unroll
+        for (int k = 0; k < kJoinAtOnce; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!(g[k] < 0.f)) o[i] += g[k] * v[k][i];
       }
     }
     if (ONE) {
-      __syncthreads();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int d = i * 128 + l * 4;
         if (d < a.dim) *(f32x4*)&red[grp][d] = o[i];
       }
       __syncthreads();
-      if (grp) continue;
+      if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int d = i * 128 + l * 4;
+          if (d < a.dim)
+            for (int k = 1; k < 8; ++k) o[i] += *(const f32x4*)&red[k][d];
+        }
+      }
+    }
+    if (live && (!ONE || grp == 0)) {
+      const float inv = weight == 0.f ? 0.f : 1.f / weight;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int d = i * 128 + l * 4;
-        if (d < a.dim)
-          for (int k = 1; k < 8; ++k) o[i] += *(const f32x4*)&red[k][d];
+        if (d >= a.dim) continue;
+        const f32x4 v = weight == 0.f ? f32x4{} : o[i] * inv;
+        const int64_t at = (int64_t)t * a.ldy + h * a.dim + d;
+        if (a.y_bf16)
+          *(u32x2*)((uint16_t*)a.y + at) = u32x2{pack(v.x, v.y), pack(v.z, v.w)};
+        else
+          *(f32x4*)((float*)a.y + at) = v;
       }
+      if (a.lse && l == 0) a.lse[row] = weight == 0.f ? kNone : (m + __builtin_log2f(weight)) * kLn2;
     }
-    if (!live) continue;
-    const float f = weight == 0.f ? 0.f : 1.f / weight;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int d = i * 128 + l * 4;
-      if (d >= a.dim) continue;
-      const f32x4 v = weight == 0.f ? f32x4{} : o[i] * f;
-      const int64_t at = (int64_t)t * a.ldy + h * a.dim + d;
-      if (a.y_bf16)
-        *(u32x2*)((uint16_t*)a.y + at) = u32x2{pack(v.x, v.y), pack(v.z, v.w)};
-      else
-        *(f32x4*)((float*)a.y + at) = v;
-    }
-    if (a.lse && l == 0) a.lse[row] = weight == 0.f ? kNone : (m + __builtin_log2f(weight)) * kLn2;
+    if (ONE) __syncthreads();
   }
 }
 
@@ -79,6 +129,7 @@ AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_h
   AttendPlan p;
   const int64_t group = heads / kv_heads, per = kAttendRows;
   p.wide = max_tokens * group > 32;
+  p.rows = (int32_t)(max_tokens * group);
   int64_t tiles = seqs;
   if (p.wide) {
     const int64_t most = tokens * group / per + seqs;
@@ -86,13 +137,15 @@ AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_h
     if (tiles > most) tiles = most;
   }
   const int64_t groups = tiles * kv_heads, blocks = (max_length + 31) / 32;
-  const int64_t want = p.wide ? 512 : 2048, least = p.wide ? 16 : 8;  // workgroups; blocks of a part
+  const int64_t want = p.wide ? 512 : 256, least = p.wide ? 16 : 8;  // workgroups; blocks of a part
   int64_t splits = (want + groups - 1) / groups;
   const int64_t most = blocks / least > 1 ? blocks / least : 1;
   if (splits > most) splits = most;
+  if (!p.wide && blocks <= 48) splits = 1;
   if (splits > 256) splits = 256;
   int64_t chunk = (blocks + splits - 1) / splits;
-  chunk = (chunk + kWaves - 1) / kWaves * kWaves;
+  const int64_t whole = p.wide ? 4 : kFewWaves;
+  chunk = (chunk + whole - 1) / whole * whole;
   p.chunk = (int32_t)chunk;
   p.splits = (int32_t)((blocks + chunk - 1) / chunk);
   p.bytes = p.splits > 1 ? size_t(p.splits) * size_t(tokens) * heads * (dim + 2) * 4 : 0;
@@ -101,13 +154,15 @@ AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_h
 
 hipError_t launch_attend(const AttendArgs& args, const AttendPlan& p, hipStream_t s) {
   AttendArgs a = args;
+  a.rows = p.rows;
   a.splits = p.splits;
   a.chunk = p.chunk;
   const hipError_t e = p.wide ? launch_attend_many(a, s) : launch_attend_few(a, s);
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = (int64_t)a.tokens * a.heads, groups = a.splits > 16 ? rows : (rows + 7) / 8;
+  const bool one = a.splits > 8;
+  const int64_t rows = (int64_t)a.tokens * a.heads, groups = one ? rows : (rows + 7) / 8;
   const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-  if (a.splits > 16)
+  if (one)
     hipLaunchKernelGGL(attend_join_kernel<true>, grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL(attend_join_kernel<false>, grid, dim3(256), 0, s, a);

@@ -27,7 +27,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -INFINITY;
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;     // of a workgroup with many rows
+constexpr int kFewWaves = 8;  // with few
 // A row's maximum moves only when a score is this far above it (in powers of two):
 // weights stay below 2^8, and most blocks leave the sums as they are.
 constexpr float kSlack = 8.f;
@@ -52,7 +53,7 @@ __device__ __forceinline__ int32_t scalar(const int32_t* p, int64_t i) {
   return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[i];
 }
 
-// Key of register i of S^T, less 4 (lane / 32).
+// Key of register i of S^T, less the lane's first, 4 (lane / 32).
 __device__ __forceinline__ constexpr int key_of(int i) { return 8 * (i / 4) + i % 4; }
 
 struct Seq {
@@ -136,19 +137,35 @@ __device__ __forceinline__ int wave_min(int v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 
-__device__ __forceinline__ Range range_of(const AttendArgs& a, const Seq& s, const Row& r) {
-  // (of a tree, drafted keys below the lower bound of the context may be seen: their
-  // distance goes by their depth)
-  const int top = a.mask ? s.start : r.upper;
-  const int low = a.mask && r.lower > s.start ? s.start : r.lower;
-  const bool any = low < r.upper;
+template <int N>
+__device__ __forceinline__ Range range_of(const AttendArgs& a, const Seq& s, const Row (&rows)[N]) {
+  int lo = 1 << 30, hi = 0, lo_all = 0, hi_all = 1 << 30;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Row& r = rows[i];
+    // (of a tree, drafted keys below the lower bound of the context may be seen: their
+    // distance goes by their depth)
+    int top = a.mask ? s.start : r.upper;
+    if (a.slopes && r.pos + 1 < top) top = r.pos + 1;
+    const int low = a.mask && r.lower > s.start ? s.start : r.lower;
+    if (low < r.upper) {
+      lo = low < lo ? low : lo;
+      hi = r.upper > hi ? r.upper : hi;
+    }
+    lo_all = r.lower > lo_all ? r.lower : lo_all;
+    hi_all = top < hi_all ? top : hi_all;
+  }
   Range g;
-  g.lo = wave_min(any ? low : 1 << 30);
-  g.hi = -wave_min(any ? -r.upper : 0);
-  g.lo_all = -wave_min(-r.lower);
-  g.hi_all = wave_min(a.slopes && r.pos + 1 < top ? r.pos + 1 : top);
+  g.lo = wave_min(lo);
+  g.hi = -wave_min(-hi);
+  g.lo_all = -wave_min(-lo_all);
+  g.hi_all = wave_min(hi_all);
   if (g.lo < 0) g.lo = 0;
   return g;
+}
+__device__ __forceinline__ Range range_of(const AttendArgs& a, const Seq& s, const Row& r) {
+  const Row one[1] = {r};
+  return range_of<1>(a, s, one);
 }
 
 // Bits j .. j + 31 of a row of the mask (bits outside it are 0).
@@ -197,38 +214,38 @@ struct Cap {
 // Scores of a block in powers of two (without a cap or slopes they stay products, which
 // a factor turns into such).  ALL: every row sees all of its keys and stands behind
 // them; else x of keys that the row does not see becomes -inf.
-template <int MODE, bool ALL>
-__device__ __forceinline__ void scores(const AttendArgs& a, const Seq& s, const Row& r, int kb, int half, f32x16& x) {
-  const int k0 = kb + 4 * half;
+template <int MODE, bool ALL, int N, typename X>
+__device__ __forceinline__ void scores(const AttendArgs& a, const Seq& s, const Row& r, int kb, int lane_key, X& x) {
+  const int k0 = kb + lane_key;
   if (MODE & kCap) {
     const Cap cap(a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = cap(x[i]);
+    for (int i = 0; i < N; ++i) x[i] = cap(x[i]);
   }
   if (MODE & kSlopes) {
     const float sc = MODE & kCap ? 1.f : a.scale * kLog2e;
     if (ALL || (!a.prefix && !a.mask)) {  // (no key that the row sees is ahead of it)
       const float base = -r.slope * (float)(r.pos - k0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], sc, __builtin_fmaf(r.slope, (float)key_of(i), base));
+      for (int i = 0; i < N; ++i) x[i] = __builtin_fmaf(x[i], sc, __builtin_fmaf(r.slope, (float)key_of(i), base));
     } else {
       const float d = (float)(r.pos - k0);
       const float slope = a.mask && kb + 32 > s.start ? 0.f : r.slope;  // (drafted keys: below)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * sc - slope * __builtin_fabsf(d - (float)key_of(i));
+      for (int i = 0; i < N; ++i) x[i] = x[i] * sc - slope * __builtin_fabsf(d - (float)key_of(i));
     }
   }
   if (ALL) return;
   if (a.mask && kb + 32 > s.start) {  // a block of drafted keys
-    const uint32_t bits = mask_bits(a, r.token, kb - s.start) >> (4 * half);
+    const uint32_t bits = mask_bits(a, r.token, kb - s.start) >> lane_key;
     const bool far = a.window > 0 || a.slopes;
     const int pos = far ? key_pos(a, s, kb + (int)(threadIdx.x & 31)) : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int k = k0 + key_of(i);
       bool in = k < r.upper && (k < s.start ? k >= r.lower : (bits >> key_of(i) & 1) && k >= r.first);
       if (far) {
-        const int d = r.pos - __shfl(pos, 4 * half + key_of(i), 64);
+        const int d = r.pos - __shfl(pos, lane_key + key_of(i), 64);
         in = in && (a.window == 0 || d < a.window);
         if (MODE & kSlopes) x[i] -= r.slope * __builtin_fabsf((float)d);
       }
@@ -238,7 +255,7 @@ __device__ __forceinline__ void scores(const AttendArgs& a, const Seq& s, const 
   }
   const int lower = r.lower - k0, upper = r.upper - k0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < N; ++i)
     if (key_of(i) < lower || key_of(i) >= upper) x[i] = kNone;
 }
 
@@ -298,7 +315,7 @@ struct Odd {
 template <int D, int MODE, bool ALL, bool TAME, typename V>
 __device__ __forceinline__ void take(const AttendArgs& a, const Seq& s, const Row& r, const Range& g, float sc, int kb,
                                      int half, f32x16& x, bool hidden, Sums<D>& c, Odd& odd, const V& value) {
-  scores<MODE, ALL>(a, s, r, kb, half, x);
+  scores<MODE, ALL, 16>(a, s, r, kb, 4 * half, x);
   if (!ALL && hidden) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = kNone;
@@ -378,7 +395,7 @@ __device__ __forceinline__ void settle(const AttendArgs& a, const Seq& s, const 
     int64_t at;
     if (!block_at(a, s, kvh, blk, D, at)) continue;
     f32x16 x = {};
-    scores<MODE, false>(a, s, r, kb, half, x);
+    scores<MODE, false, 16>(a, s, r, kb, 4 * half, x);
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 16; i += 2) w[i / 2] = (x[i] == kNone ? 0u : 0x3F80u) | (x[i + 1] == kNone ? 0u : 0x3F800000u);
@@ -405,14 +422,13 @@ __device__ __forceinline__ void settle(const AttendArgs& a, const Seq& s, const 
 }
 
 // Whether some row's sums are not finite.
-template <int D>
-__device__ __forceinline__ bool not_finite(const Sums<D>& c) {
-  // (a value less itself is not zero then; so neither is the sum of such)
-  float v = c.l - c.l;
+template <int N, typename O>
+__device__ __forceinline__ bool not_finite(const O (&o)[N], int each) {
+  float v = 0.f;  // (a value less itself is not zero then; so neither is the sum of such)
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t)
+  for (int t = 0; t < N; ++t)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += c.o[t][i] - c.o[t][i];
+    for (int i = 0; i < each; ++i) v += o[t][i] - o[t][i];
   return __ballot(v != 0.f) != 0;
 }
 
@@ -428,7 +444,8 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Row& r, in
 // the part's place.
 __device__ __forceinline__ void put(const AttendArgs& a, const Row& r, int z, int d, f32x4 o, float weight) {
   if (a.splits > 1) {
-    *(f32x4*)(a.part + (((int64_t)z * a.tokens + r.token) * a.heads + r.head) * a.dim + d) = o;
+    if (weight != 0.f)  // (else the join passes it by)
+      *(f32x4*)(a.part + (((int64_t)z * a.tokens + r.token) * a.heads + r.head) * a.dim + d) = o;
     return;
   }
   const float f = weight == 0.f ? 0.f : 1.f / weight;
@@ -483,6 +500,20 @@ __device__ __attribute__((noinline)) void careful(const AttendArgs* args, int b,
     if (odd.last >= 0) settle<D, MODE>(a, s, r, g, kvh, half, odd, step, c);
   }
   *out = c;
+}
+
+// A wave's sums to their places.
+template <int D>
+__device__ __forceinline__ void put_all(const AttendArgs& a, const Row& r, int z, int half, Sums<D>& c) {
+  c.l += other_half(c.l);
+  if (!r.live) return;
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      put(a, r, z, t * 32 + 8 * i + 4 * half, f32x4{c.o[t][4 * i], c.o[t][4 * i + 1], c.o[t][4 * i + 2], c.o[t][4 * i + 3]},
+          c.l);
+  if (half == 0) put_row(a, r, z, c.m, c.l);
 }
 
 // (of a kernel, whose only argument an AttendArgs is)

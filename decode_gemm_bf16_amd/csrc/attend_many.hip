@@ -322,21 +322,13 @@ __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kern
     }
     arrive();  // (of tiles behind the end, too: nothing is written to LDS later on)
   }
-  if (not_finite(c)) {
+  if (not_finite(c.o, 16)) {
     Sums<D> again;
     careful<D, MODE>(kernel_args(), b, kvh, rt * kManyRows + w * 32, b0 + z * a.chunk, a.chunk, a.splits * a.chunk, b1, 0, 1,
                      &again);
     c = again;
   }
-  c.l += other_half(c.l);
-  if (!r.live) return;
-#pragma unroll
-  for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      put(a, r, z, t * 32 + 8 * i + 4 * half, f32x4{c.o[t][4 * i], c.o[t][4 * i + 1], c.o[t][4 * i + 2], c.o[t][4 * i + 3]},
-          c.l);
-  if (half == 0) put_row(a, r, z, c.m, c.l);
+  put_all(a, r, z, half, c);
 }
 
 template <int D, int MODE>

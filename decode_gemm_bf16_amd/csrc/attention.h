@@ -70,6 +70,7 @@ struct AttendArgs {
   float* part;   // [splits][tokens * heads][dim] sums, then [splits][tokens * heads][2] maximum and weight
   int64_t ldq, ldy, ldt;
   int32_t tokens, seqs, heads, kv_heads, group, dim, page_log2, pages, max_pages, words, window;
+  int32_t rows;    // of one sequence and head of the cache that the call is laid out for
   int32_t splits;  // parts of the keys
   int32_t chunk;   // blocks of 32 keys a part
   float scale, cap;
@@ -80,7 +81,7 @@ constexpr int kAttendRows = 128;
 // The rule on sizes that chooses kernel and parts.
 struct AttendPlan {
   bool wide;  // kAttendRows a workgroup, else 32
-  int32_t splits, chunk;
+  int32_t rows, splits, chunk;
   size_t bytes;  // of the workspace
 };
 AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
