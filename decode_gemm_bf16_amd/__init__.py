@@ -32,7 +32,9 @@ EXPORTED = [
     "uw_route", "uw_group_rows_workspace_bytes", "uw_group_rows", "uw_dispatch_rows", "uw_combine_rows",
     "uw_moe_workspace_bytes", "uw_moe_forward", "uw_lora_create", "uw_lora_load", "uw_lora_free", "uw_lora_plan_bytes",
     "uw_lora_plan", "uw_lora_workspace_bytes", "uw_lora_apply", "uw_cache_write", "uw_attend_workspace_bytes", "uw_attend",
-    "uw_cache_copy_pages", "uw_cache_keep", "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
+    "uw_cache_copy_pages", "uw_cache_keep", "uw_pages_create",
+    "uw_pages_free", "uw_pages_left", "uw_pages_holders", "uw_pages_take", "uw_pages_share", "uw_pages_drop", "uw_pages_own",
+    "uw_pages_compact", "uw_attention_workspace_bytes", "uw_attention_forward", "uw_stream_create", "uw_stream_destroy", "uw_device_cu_count", "uw_gemm_bf16", "uw_device_copy", "uw_device_read",
 ]
 
 F32, BF16 = 0, 1
@@ -76,6 +78,13 @@ class Rotary(C.Structure):
 
 class AttendConfig(C.Structure):
     _fields_ = [("scale", C.c_float), ("cap", C.c_float), ("window", C.c_int32)]
+
+
+class AttentionBatch(C.Structure):
+    _fields_ = ([(k, C.c_void_p) for k in ("positions", "freqs", "axis", "slots", "offsets", "lengths", "tables", "slopes",
+                                           "prefix", "first", "mask")] +
+                [(k, C.c_int64) for k in ("tokens", "seqs", "max_tokens", "max_length", "ldt", "max_pages")] +
+                [("mask_words", C.c_int32)])
 
 
 def _preload_runtime() -> None:
@@ -149,6 +158,18 @@ def _load() -> C.CDLL:
                        vp, vp, i32, i64, i64, i64, i64, vp, i64, i32, vp, vp, C.c_size_t, vp], st),
         "uw_cache_copy_pages": ([C.POINTER(CacheConfig), i64, vp, vp, vp, vp, i64, vp], st),
         "uw_cache_keep": ([C.POINTER(CacheConfig), i64, vp, vp, vp, i64, i64, vp, vp, i32, i64, vp, vp], st),
+        "uw_pages_create": ([i64, C.POINTER(vp)], st),
+        "uw_pages_free": ([vp], None),
+        "uw_pages_left": ([vp], i64),
+        "uw_pages_holders": ([vp, i32], i32),
+        "uw_pages_take": ([vp, i64, vp], st),
+        "uw_pages_share": ([vp, vp, i64], st),
+        "uw_pages_drop": ([vp, vp, i64], st),
+        "uw_pages_own": ([vp, i32, C.POINTER(i32)], st),
+        "uw_pages_compact": ([vp, vp, vp, C.POINTER(i64)], st),
+        "uw_attention_workspace_bytes": ([C.POINTER(CacheConfig), i64, i64, i64, i64], C.c_size_t),
+        "uw_attention_forward": ([vp, vp, vp, vp, C.POINTER(i32), C.POINTER(CacheConfig), C.POINTER(Rotary),
+                                  C.POINTER(AttendConfig), C.POINTER(AttentionBatch), vp, vp, vp, vp, vp, C.c_size_t], st),
         "uw_stream_create": ([i32, i32, C.POINTER(vp)], st),
         "uw_stream_destroy": ([vp], st),
         "uw_device_cu_count": ([], i32),
@@ -788,3 +809,100 @@ def cache_keep(kc, vc, tables, starts, kept, lengths, stream=None) -> None:
                               _tensor(vc, "vc", _bf16, shape, dev), tp, ldt, reach,
                               _tensor(starts, "starts", _i32, (n,), dev), _tensor(kept, "kept", _i32, (n, most), dev),
                               most, n, _tensor(lengths, "lengths", _i32, (n,), dev), _stream_ptr(stream)))
+
+
+class Pages:
+    """The pages of a cache, counted on the host (a ``uw_pages``): lists of pages are
+    int32 arrays.  The rows are copied by ``cache_copy_pages``."""
+
+    def __init__(self, pages: int):
+        h = C.c_void_p()
+        self._h = h
+        _check(_lib.uw_pages_create(pages, C.byref(h)))
+        self.pages = pages
+
+    @property
+    def left(self) -> int:
+        return _lib.uw_pages_left(self._h)
+
+    def holders(self, page: int) -> int:
+        return _lib.uw_pages_holders(self._h, page)
+
+    def take(self, n: int) -> np.ndarray:
+        """The n lowest free pages."""
+        out = np.empty(max(n, 0), dtype=np.int32)
+        _check(_lib.uw_pages_take(self._h, n, out.ctypes.data))
+        return out
+
+    def share(self, pages) -> None:
+        """A fork: each page is held once more."""
+        a = np.ascontiguousarray(pages, dtype=np.int32)
+        _check(_lib.uw_pages_share(self._h, a.ctypes.data, a.size))
+
+    def drop(self, pages) -> None:
+        """Each page is held once less; free where nobody holds it."""
+        a = np.ascontiguousarray(pages, dtype=np.int32)
+        _check(_lib.uw_pages_drop(self._h, a.ctypes.data, a.size))
+
+    def own(self, page: int) -> int:
+        """The page to write in place of ``page``: itself, or a new one to copy it to."""
+        out = C.c_int32()
+        _check(_lib.uw_pages_own(self._h, page, C.byref(out)))
+        return out.value
+
+    def compact(self) -> tuple[np.ndarray, np.ndarray]:
+        """(sources, destinations) of the moves that bring the used pages together."""
+        src, dst, n = np.empty(self.pages, dtype=np.int32), np.empty(self.pages, dtype=np.int32), C.c_int64()
+        _check(_lib.uw_pages_compact(self._h, src.ctypes.data, dst.ctypes.data, C.byref(n)))
+        return src[:n.value].copy(), dst[:n.value].copy()
+
+    def free(self) -> None:
+        if self._h:
+            _lib.uw_pages_free(self._h)
+            self._h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def attention_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int, max_tokens: int,
+                              max_length: int) -> int:
+    return _lib.uw_attention_workspace_bytes(CacheConfig(heads, kv_heads, dim, 32, 1), tokens, seqs, max_tokens, max_length)
+
+
+def attention_forward(q: Matrix, k: Matrix, v: Matrix, o: Matrix, pipelines, x, y, work, kc, vc, positions, freqs, slots,
+                      offsets, lengths, tables, axis=None, adjacent: bool = False, scale: float | None = None,
+                      cap: float = 0.0, window: int = 0, slopes=None, prefix=None, first=None, mask=None,
+                      max_tokens: int | None = None, max_length: int | None = None) -> None:
+    """An attention layer on compressed projections (``uw_attention_forward``), on the
+    handles' main stream: x [tokens, hidden] bfloat16 -> y [tokens, hidden] float32; the
+    others as in ``cache_write`` and ``attend``."""
+    dev = _device()
+    shape = pages, kv, page, dim = _cache_shape(kc, 4)
+    rows = t, hidden = _shape2(x, "x")
+    if hidden != q.cols:
+        raise ValueError(f"x must have {q.cols} columns, not {hidden}")
+    heads = _heads(q.rows, dim, "q's output")
+    axes = _shape2(positions, "positions")[0]
+    pairs = freqs.numel()
+    table = n, reach = _shape2(tables, "tables")
+    tp, ldt = _rows(tables, "tables", _i32, table, dev)
+    words = 0 if mask is None else _shape2(mask, "mask")[1]
+    batch = AttentionBatch(
+        _tensor(positions, "positions", _i32, (axes, t), dev), _tensor(freqs, "freqs", _f32, (pairs,), dev),
+        None if axis is None else _tensor(axis, "axis", _i32, (pairs,), dev), _tensor(slots, "slots", _i32, (t,), dev),
+        _tensor(offsets, "offsets", _i32, (n + 1,), dev), _tensor(lengths, "lengths", _i32, (n,), dev), tp,
+        None if slopes is None else _tensor(slopes, "slopes", _f32, (heads,), dev),
+        None if prefix is None else _tensor(prefix, "prefix", _i32, (n,), dev),
+        None if first is None else _tensor(first, "first", _i32, (t,), dev),
+        None if mask is None else _tensor(mask, "mask", _i64, (t, words), dev), t, n,
+        t if max_tokens is None else max_tokens, reach * page if max_length is None else max_length, ldt, reach, words)
+    wp, wb = _bytes(work, "work", dev)
+    _check(_lib.uw_attention_forward(q._h, k._h, v._h, o._h, (C.c_int32 * 4)(*pipelines),
+                                     _cache_config(heads, kv, dim, page, pages), _rotary(axes, pairs, adjacent),
+                                     _attend_config(dim ** -0.5 if scale is None else scale, cap, window), batch,
+                                     _tensor(x, "x", _bf16, rows, dev), _tensor(kc, "kc", _bf16, shape, dev),
+                                     _tensor(vc, "vc", _bf16, shape, dev), _tensor(y, "y", _f32, rows, dev), wp, wb))

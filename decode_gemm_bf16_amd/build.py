@@ -19,7 +19,7 @@ OUT = os.path.join(HERE, "libuw.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["codec.cpp", "runtime.cpp", "variants.cpp", "fused_small.hip", "fused_mid.hip", "fused_large.hip", "fused_ring.hip", "fused_wide.hip", "fused_rowk.hip", "transcode.hip",
-           "huff_decode.hip", "misc.hip", "noalloc.hip", "route.hip", "rows.hip", "lora.hip", "routing.cpp", "cache.hip", "attend.hip", "attend_few.hip", "attend_many.hip", "attention.cpp"]
+           "huff_decode.hip", "misc.hip", "noalloc.hip", "route.hip", "rows.hip", "lora.hip", "routing.cpp", "cache.hip", "attend.hip", "attend_few.hip", "attend_many.hip", "attention.cpp", "pages.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

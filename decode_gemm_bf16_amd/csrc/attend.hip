@@ -8,9 +8,8 @@ namespace {
 //
 // A workgroup joins 8 rows, 32 lanes each, or one row whose parts its 8 groups of 32
 // lanes divide (ONE).  Up to 32 parts, and 256: a lane has each part's maximum and weight;
-// then 4 elements of 32 columns a lane, 4 parts' loads in flight.
-constexpr int kJoinAtOnce = 4;
-
+// then 4 elements of 32 columns a lane (H: twice, of long heads), the loads of
+// several parts in flight.
 __device__ __forceinline__ float max32(float v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, 64));
@@ -22,8 +21,9 @@ __device__ __forceinline__ float sum32(float v) {
   return v;
 }
 
-template <bool ONE>
+template <bool ONE, int H>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
+  constexpr int kJoinAtOnce = ONE ? 4 : 2;
   __shared__ __attribute__((aligned(16))) float red[8][256];
   __shared__ float factor[256], tops[8], weights[8];
   const int grp = threadIdx.x >> 5, l = threadIdx.x & 31;
@@ -57,12 +57,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) weight += weights[k];
     }
-    f32x4 o[2] = {};
+    f32x4 o[H] = {};
     const float* const part = a.part + row * a.dim;
     const int step = ONE ? 8 : 1;
     if (live) {
       for (int z0 = ONE ? grp : 0; z0 < a.splits; z0 += step * kJoinAtOnce) {
-        f32x4 v[kJoinAtOnce][2];
+        f32x4 v[kJoinAtOnce][H];
         float g[kJoinAtOnce];
 #pragma unroll
         for (int k = 0; k < kJoinAtOnce; ++k) {
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
             g[k] = __shfl(there ? f : -1.f, (threadIdx.x & 32) + (z < 32 ? z : 31), 64);
           if (z >= a.splits) g[k] = -1.f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < H; ++i) {
             const int d = i * 128 + l * 4;
             v[k][i] = f32x4{};
             if (d < a.dim && !(g[k] < 0.f)) v[k][i] = *(const f32x4*)(part + (int64_t)z * rows * a.dim + d);
@@ -82,20 +82,20 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
         for (int k = 0; k < kJoinAtOnce; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < H; ++i)
             if (!(g[k] < 0.f)) o[i] += g[k] * v[k][i];
       }
     }
     if (ONE) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < H; ++i) {
         const int d = i * 128 + l * 4;
         if (d < a.dim) *(f32x4*)&red[grp][d] = o[i];
       }
       __syncthreads();
       if (grp == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < H; ++i) {
           const int d = i * 128 + l * 4;
           if (d < a.dim)
             for (int k = 1; k < 8; ++k) o[i] += *(const f32x4*)&red[k][d];
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     if (live && (!ONE || grp == 0)) {
       const float inv = weight == 0.f ? 0.f : 1.f / weight;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < H; ++i) {
         const int d = i * 128 + l * 4;
         if (d >= a.dim) continue;
         const f32x4 v = weight == 0.f ? f32x4{} : o[i] * inv;
@@ -119,6 +119,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     }
     if (ONE) __syncthreads();
   }
+}
+
+template <bool ONE, int H>
+void join(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  hipLaunchKernelGGL((attend_join_kernel<ONE, H>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -162,10 +167,10 @@ hipError_t launch_attend(const AttendArgs& args, const AttendPlan& p, hipStream_
   const bool one = a.splits > 8;
   const int64_t rows = (int64_t)a.tokens * a.heads, groups = one ? rows : (rows + 7) / 8;
   const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-  if (one)
-    hipLaunchKernelGGL(attend_join_kernel<true>, grid, dim3(256), 0, s, a);
+  if (a.dim > 128)
+    one ? join<true, 2>(a, grid, s) : join<false, 2>(a, grid, s);
   else
-    hipLaunchKernelGGL(attend_join_kernel<false>, grid, dim3(256), 0, s, a);
+    one ? join<true, 1>(a, grid, s) : join<false, 1>(a, grid, s);
   return hipGetLastError();
 }
 

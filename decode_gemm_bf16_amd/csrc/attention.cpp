@@ -120,21 +120,21 @@ uw_status check_attend_sizes(int64_t tokens, int64_t seqs, int32_t heads, int32_
 
 }  // namespace
 
-extern "C" {
+namespace uw {
 
-uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
-                         const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
-                         const int32_t* positions_dev, const float* freqs_dev, const int32_t* axis_dev,
-                         const int32_t* slots_dev, int64_t tokens, uint16_t* q_out_dev, int64_t ldq_out,
-                         uint16_t* k_cache_dev, uint16_t* v_cache_dev, void* stream) {
+uw_status cache_write_prepare(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
+                              const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
+                              const int32_t* positions_dev, const float* freqs_dev, const int32_t* axis_dev,
+                              const int32_t* slots_dev, int64_t tokens, uint16_t* q_out_dev, int64_t ldq_out,
+                              uint16_t* k_cache_dev, uint16_t* v_cache_dev, CacheWriteArgs* out) {
   uw_status st = check_cache(config, k_cache_dev, v_cache_dev);
   if (st != UW_OK) return st;
   const uw_cache_config& c = *config;
   if (!rotary || !k_dev || !v_dev || !slots_dev || (q_dev && !q_out_dev)) return fail(UW_ERR_INVALID_ARG, "null argument");
   if ((q_dev && (st = check_heads(config)) != UW_OK) || (st = check_tokens(tokens)) != UW_OK) return st;
   if (type != UW_F32 && type != UW_BF16) return fail(UW_ERR_INVALID_ARG, "unknown type %d", type);
-  if (rotary->axes < 1 || rotary->axes > uw::kRotaryMaxAxes)
-    return fail(UW_ERR_INVALID_ARG, "axes = %d must be 1..%d", rotary->axes, uw::kRotaryMaxAxes);
+  if (rotary->axes < 1 || rotary->axes > kRotaryMaxAxes)
+    return fail(UW_ERR_INVALID_ARG, "axes = %d must be 1..%d", rotary->axes, kRotaryMaxAxes);
   if (rotary->pairs < 0 || rotary->pairs > c.dim / 2)
     return fail(UW_ERR_SHAPE, "pairs = %d must be 0..%d", rotary->pairs, c.dim / 2);
   if (rotary->pairs > 0 && (!positions_dev || !freqs_dev)) return fail(UW_ERR_INVALID_ARG, "null positions or frequencies");
@@ -159,7 +159,7 @@ uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary,
                         {turn ? axis_dev : nullptr, np},
                         {slots_dev, size_t(tokens) * 4}};
   if ((st = check_apart(spans, 3, 10)) != UW_OK) return st;
-  uw::CacheWriteArgs a;
+  CacheWriteArgs& a = *out;
   a.q = q_dev;
   a.k = k_dev;
   a.v = v_dev;
@@ -184,27 +184,16 @@ uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary,
   a.pairs = rotary->pairs;
   a.adjacent = rotary->adjacent != 0;
   a.bf16 = type == UW_BF16;
-  UW_HIP(uw::launch_cache_write(a, static_cast<hipStream_t>(stream)));
   return UW_OK;
 }
 
-size_t uw_attend_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
-                                 int64_t max_tokens, int64_t max_length) {
-  const uw_cache_config c = {heads, kv_heads, dim, 32, 1};
-  if (check_cache(&c, &c, &c) == UW_ERR_SHAPE || check_heads(&c) != UW_OK || check_tokens(tokens) != UW_OK ||
-      check_sequences(seqs, 1, 1) != UW_OK ||
-      check_attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length) != UW_OK)
-    return 0;
-  return uw::attend_plan(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length).bytes;
-}
-
-uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* options, const uint16_t* q_dev, int64_t ldq,
-                    const uint16_t* k_cache_dev, const uint16_t* v_cache_dev, const int32_t* offsets_dev,
-                    const int32_t* lengths_dev, const int32_t* tables_dev, int64_t ldt, int64_t max_pages,
-                    const float* slopes_dev, const int32_t* prefix_dev, const int32_t* first_dev,
-                    const uint64_t* mask_dev, int32_t mask_words, int64_t tokens, int64_t seqs, int64_t max_tokens,
-                    int64_t max_length, void* y_dev, int64_t ldy, int32_t y_type, float* lse_dev, void* work_dev,
-                    size_t work_bytes, void* stream) {
+uw_status attend_prepare(const uw_cache_config* config, const uw_attend_config* options, const uint16_t* q_dev,
+                         int64_t ldq, const uint16_t* k_cache_dev, const uint16_t* v_cache_dev, const int32_t* offsets_dev,
+                         const int32_t* lengths_dev, const int32_t* tables_dev, int64_t ldt, int64_t max_pages,
+                         const float* slopes_dev, const int32_t* prefix_dev, const int32_t* first_dev,
+                         const uint64_t* mask_dev, int32_t mask_words, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                         int64_t max_length, void* y_dev, int64_t ldy, int32_t y_type, float* lse_dev, void* work_dev,
+                         size_t work_bytes, AttendArgs* out, AttendPlan* plan_out) {
   uw_status st = check_cache(config, k_cache_dev, v_cache_dev);
   if (st != UW_OK) return st;
   const uw_cache_config& c = *config;
@@ -227,7 +216,8 @@ uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* optio
   if (!aligned(offsets_dev, 4) || !aligned(lengths_dev, 4) || !aligned(tables_dev, 4) || !aligned(slopes_dev, 4) ||
       !aligned(prefix_dev, 4) || !aligned(first_dev, 4) || !aligned(mask_dev, 8) || !aligned(lse_dev, 4))
     return fail(UW_ERR_INVALID_ARG, "misaligned pointer");
-  const uw::AttendPlan plan = uw::attend_plan(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length);
+  AttendPlan& plan = *plan_out;
+  plan = attend_plan(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length);
   if (plan.bytes && (!work_dev || work_bytes < plan.bytes))
     return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, the call needs %zu", work_dev ? work_bytes : size_t(0), plan.bytes);
   if (plan.bytes && !aligned(work_dev, 16)) return fail(UW_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
@@ -245,7 +235,7 @@ uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* optio
                         {first_dev, size_t(tokens) * 4},
                         {mask_dev, size_t(tokens) * size_t(mask_dev ? mask_words : 0) * 8}};
   if ((st = check_apart(spans, 3, 13)) != UW_OK) return st;
-  uw::AttendArgs a;
+  AttendArgs& a = *out;
   a.q = q_dev;
   a.kc = k_cache_dev;
   a.vc = v_cache_dev;
@@ -276,6 +266,51 @@ uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* optio
   a.scale = options->scale;
   a.cap = options->cap;
   a.y_bf16 = y_type == UW_BF16;
+  return UW_OK;
+}
+
+}  // namespace uw
+
+extern "C" {
+
+uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
+                         const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
+                         const int32_t* positions_dev, const float* freqs_dev, const int32_t* axis_dev,
+                         const int32_t* slots_dev, int64_t tokens, uint16_t* q_out_dev, int64_t ldq_out,
+                         uint16_t* k_cache_dev, uint16_t* v_cache_dev, void* stream) {
+  uw::CacheWriteArgs a;
+  const uw_status st = uw::cache_write_prepare(config, rotary, q_dev, ldq, k_dev, ldk, v_dev, ldv, type, positions_dev,
+                                               freqs_dev, axis_dev, slots_dev, tokens, q_out_dev, ldq_out, k_cache_dev,
+                                               v_cache_dev, &a);
+  if (st != UW_OK) return st;
+  UW_HIP(uw::launch_cache_write(a, static_cast<hipStream_t>(stream)));
+  return UW_OK;
+}
+
+size_t uw_attend_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                                 int64_t max_tokens, int64_t max_length) {
+  const uw_cache_config c = {heads, kv_heads, dim, 32, 1};
+  if (check_cache(&c, &c, &c) == UW_ERR_SHAPE || check_heads(&c) != UW_OK || check_tokens(tokens) != UW_OK ||
+      check_sequences(seqs, 1, 1) != UW_OK ||
+      check_attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length) != UW_OK)
+    return 0;
+  return uw::attend_plan(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length).bytes;
+}
+
+uw_status uw_attend(const uw_cache_config* config, const uw_attend_config* options, const uint16_t* q_dev, int64_t ldq,
+                    const uint16_t* k_cache_dev, const uint16_t* v_cache_dev, const int32_t* offsets_dev,
+                    const int32_t* lengths_dev, const int32_t* tables_dev, int64_t ldt, int64_t max_pages,
+                    const float* slopes_dev, const int32_t* prefix_dev, const int32_t* first_dev,
+                    const uint64_t* mask_dev, int32_t mask_words, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                    int64_t max_length, void* y_dev, int64_t ldy, int32_t y_type, float* lse_dev, void* work_dev,
+                    size_t work_bytes, void* stream) {
+  uw::AttendArgs a;
+  uw::AttendPlan plan;
+  const uw_status st = uw::attend_prepare(
+      config, options, q_dev, ldq, k_cache_dev, v_cache_dev, offsets_dev, lengths_dev, tables_dev, ldt, max_pages,
+      slopes_dev, prefix_dev, first_dev, mask_dev, mask_words, tokens, seqs, max_tokens, max_length, y_dev, ldy, y_type,
+      lse_dev, work_dev, work_bytes, &a, &plan);
+  if (st != UW_OK) return st;
   UW_HIP(uw::launch_attend(a, plan, static_cast<hipStream_t>(stream)));
   return UW_OK;
 }

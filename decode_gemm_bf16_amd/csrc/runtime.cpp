@@ -1351,6 +1351,124 @@ uw_status uw_grouped_matmul(const uw_handle* experts, int32_t n, const uint16_t*
 
 namespace {
 
+// The parts of uw_attention_forward's workspace.
+struct AttentionParts {
+  size_t q, k, v, turned, y, attend, attend_bytes, total;
+};
+AttentionParts attention_parts(const uw_cache_config& c, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                               int64_t max_length) {
+  const size_t nq = size_t(tokens) * c.heads * c.dim, nk = size_t(tokens) * c.kv_heads * c.dim;
+  AttentionParts p;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  p.q = take(nq * 4);
+  p.k = take(nk * 4);
+  p.v = take(nk * 4);
+  p.turned = take(nq * 2);
+  p.y = take(nq * 2);
+  p.attend_bytes = uw::attend_plan(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length).bytes;
+  p.attend = take(p.attend_bytes);
+  p.total = at;
+  return p;
+}
+
+uw_status attention_impl(uw_handle q, uw_handle k, uw_handle v, uw_handle o, const int32_t* pipelines,
+                         const uw_cache_config* config, const uw_rotary* rotary, const uw_attend_config* options,
+                         const uw_attention_batch* batch, const uint16_t* x, uint16_t* kc, uint16_t* vc, float* y,
+                         void* work, size_t work_bytes) {
+  if (!q || !k || !v || !o || !pipelines || !config || !batch || !x || !y || !work)
+    return fail(UW_ERR_INVALID_ARG, "null argument");
+  const uw_attention_batch& b = *batch;
+  const int64_t hidden = q->cols, nq = int64_t(config->heads) * config->dim, nk = int64_t(config->kv_heads) * config->dim;
+  if (q->rows != nq || k->rows != nk || v->rows != nk || k->cols != hidden || v->cols != hidden || o->rows != hidden ||
+      o->cols != nq)
+    return fail(UW_ERR_SHAPE, "q [heads * dim, hidden], k and v [kv_heads * dim, hidden], o [hidden, heads * dim] disagree");
+  const uw_handle hs[4] = {q, k, v, o};
+  for (int j = 1; j < 4; ++j)
+    if (hs[j]->main != q->main) return fail(UW_ERR_INVALID_ARG, "q, k, v and o must share one main stream");
+  const size_t need = uw_attention_workspace_bytes(config, b.tokens, b.seqs, b.max_tokens, b.max_length);
+  if (need == 0) return fail(UW_ERR_INVALID_ARG, "tokens, seqs, max_tokens, max_length or heads out of range");
+  const uintptr_t wa = reinterpret_cast<uintptr_t>(work), xa = reinterpret_cast<uintptr_t>(x),
+                  ya = reinterpret_cast<uintptr_t>(y), ka = reinterpret_cast<uintptr_t>(kc),
+                  va = reinterpret_cast<uintptr_t>(vc);
+  if (wa % 256) return fail(UW_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+  if (xa % 16 || ya % 16) return fail(UW_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
+  if (work_bytes < need)
+    return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, the layer needs %zu", work_bytes, need);
+  int ps[4];
+  uw::Variant vs[4];
+  uw_status st;
+  for (int j = 0; j < 4; ++j)
+    if ((st = matmul_check(hs[j], x, y, b.tokens, pipelines[j], &ps[j], &vs[j])) != UW_OK) return st;
+  const AttentionParts p = attention_parts(*config, b.tokens, b.seqs, b.max_tokens, b.max_length);
+  uint8_t* const m = static_cast<uint8_t*>(work);
+  float *qf = reinterpret_cast<float*>(m + p.q), *kf = reinterpret_cast<float*>(m + p.k),
+        *vf = reinterpret_cast<float*>(m + p.v);
+  uint16_t *turned = reinterpret_cast<uint16_t*>(m + p.turned), *rows = reinterpret_cast<uint16_t*>(m + p.y);
+  // (their checks hold the caches and the indexes against the workspace's parts)
+  uw::CacheWriteArgs write;
+  uw::AttendArgs attend;
+  uw::AttendPlan plan;
+  if ((st = uw::cache_write_prepare(config, rotary, qf, nq, kf, nk, vf, nk, UW_F32, b.positions, b.freqs, b.axis, b.slots,
+                                    b.tokens, turned, nq, kc, vc, &write)) != UW_OK ||
+      (st = uw::attend_prepare(config, options, turned, nq, kc, vc, b.offsets, b.lengths, b.tables, b.ldt, b.max_pages,
+                               b.slopes, b.prefix, b.first, b.mask, b.mask_words, b.tokens, b.seqs, b.max_tokens,
+                               b.max_length, rows, nq, UW_BF16, nullptr, m + p.attend, p.attend_bytes, &attend,
+                               &plan)) != UW_OK)
+    return st;
+  struct Span {
+    uintptr_t at;
+    size_t bytes;
+  };
+  const size_t cb = size_t(config->pages) * config->kv_heads * config->page * config->dim * 2, t = size_t(b.tokens),
+               n = size_t(b.seqs);
+  const Span work_span = {wa, need}, y_span = {ya, t * hidden * 4}, caches[2] = {{ka, cb}, {va, cb}};
+  const Span ins[] = {{xa, t * hidden * 2},
+                      {reinterpret_cast<uintptr_t>(b.positions), t * rotary->axes * 4},
+                      {reinterpret_cast<uintptr_t>(b.freqs), size_t(rotary->pairs) * 4},
+                      {reinterpret_cast<uintptr_t>(b.axis), size_t(rotary->pairs) * 4},
+                      {reinterpret_cast<uintptr_t>(b.slots), t * 4},
+                      {reinterpret_cast<uintptr_t>(b.offsets), (n + 1) * 4},
+                      {reinterpret_cast<uintptr_t>(b.lengths), n * 4},
+                      {reinterpret_cast<uintptr_t>(b.tables), ((n - 1) * b.ldt + b.max_pages) * 4},
+                      {reinterpret_cast<uintptr_t>(b.slopes), size_t(config->heads) * 4},
+                      {reinterpret_cast<uintptr_t>(b.prefix), n * 4},
+                      {reinterpret_cast<uintptr_t>(b.first), t * 4},
+                      {reinterpret_cast<uintptr_t>(b.mask), b.mask ? t * b.mask_words * 8 : 0},
+                      caches[0],
+                      caches[1]};
+  auto meet = [](const Span& s, const Span& r) {
+    return s.at && r.at && s.bytes && r.bytes && s.at < r.at + r.bytes && r.at < s.at + s.bytes;
+  };
+  bool bad = meet(work_span, y_span);
+  for (const Span& in : ins) {
+    bad = bad || meet(work_span, in) || meet(y_span, in);
+    if (&in < ins + 12) bad = bad || meet(caches[0], in) || meet(caches[1], in);
+  }
+  if (bad) return fail(UW_ERR_INVALID_ARG, "y, the workspace or the cache overlaps an input or another of them");
+  const uw::Variant ek = uw::variant_effective(b.tokens, nk, hidden, false, vs[1]);
+  const uw::Variant ev = uw::variant_effective(b.tokens, nk, hidden, false, vs[2]);
+  if ((st = matmul_impl(q, x, qf, b.tokens, pipelines[0])) != UW_OK) return st;
+  if (ps[1] == 4 && ps[2] == 4 && ek.kind == 2 && ev.kind == 2 && ek.waves == ev.waves && ek.ksplit == ev.ksplit &&
+      ek.unroll == ev.unroll) {
+    const uw::FusedW ws[2] = {fused_view(k, false, k->d_nib), fused_view(v, false, v->d_nib)};
+    const uint16_t* xs[2] = {x, x};
+    float* ys[2] = {kf, vf};
+    const int64_t ts[2] = {b.tokens, b.tokens};
+    UW_HIP(uw::launch_fused_gemv_group(ws, xs, ys, ts, 2, ek, q->main));
+  } else if ((st = matmul_impl(k, x, kf, b.tokens, pipelines[1])) != UW_OK ||
+             (st = matmul_impl(v, x, vf, b.tokens, pipelines[2])) != UW_OK) {
+    return st;
+  }
+  UW_HIP(uw::launch_cache_write(write, q->main));
+  UW_HIP(uw::launch_attend(attend, plan, q->main));
+  return matmul_impl(o, rows, y, b.tokens, pipelines[3]);
+}
+
 // The parts of uw_moe_forward's workspace; n = tokens * top_k entries.
 struct MoeParts {
   size_t experts, weights, offsets, order, slot, group, xs, g, u, h, ys, total;
@@ -1486,6 +1604,24 @@ uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, con
   } catch (const std::bad_alloc&) {
     return fail(UW_ERR_OOM, "host allocation failed");
   }
+}
+
+size_t uw_attention_workspace_bytes(const uw_cache_config* config, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                                    int64_t max_length) {
+  if (!config || tokens < 1 || tokens > (int64_t(1) << 20) || config->heads < 1 || config->heads > 256 ||
+      config->kv_heads < 1 || config->kv_heads > 128 || config->dim < 1 || config->dim > 256 || max_tokens < 1 ||
+      max_tokens > tokens || max_length < 1 || max_length > (int64_t(1) << 30) || seqs < 1 || seqs > 65535 ||
+      config->heads % config->kv_heads)
+    return 0;
+  return attention_parts(*config, tokens, seqs, max_tokens, max_length).total;
+}
+
+uw_status uw_attention_forward(uw_handle q, uw_handle k, uw_handle v, uw_handle o, const int32_t* pipelines,
+                               const uw_cache_config* config, const uw_rotary* rotary, const uw_attend_config* options,
+                               const uw_attention_batch* batch, const uint16_t* x_dev, uint16_t* k_cache_dev,
+                               uint16_t* v_cache_dev, float* y_dev, void* work_dev, size_t work_bytes) {
+  return attention_impl(q, k, v, o, pipelines, config, rotary, options, batch, x_dev, k_cache_dev, v_cache_dev, y_dev,
+                        work_dev, work_bytes);
 }
 
 void uw_free(uw_handle h) {

@@ -515,8 +515,8 @@ typedef struct {
  * k_dev and v_dev [tokens, kv_heads * dim] of `type` (UW_F32, e.g. uw_matmul's
  * outputs, or UW_BF16), with row strides (multiples of 8); q may be NULL (keys and
  * values alone).  positions_dev int32 [axes, tokens]; freqs_dev float [pairs];
- * axis_dev int32 [pairs] or NULL (all 0), a pair with an axis outside 0..axes-1 is
- * not turned.  slots_dev int32 [tokens]: page * config->page + place of the token's
+ * axis_dev int32 [pairs] or NULL (all 0), an axis outside 0..axes-1 counts as
+ * position 0.  slots_dev int32 [tokens]: page * config->page + place of the token's
  * row; a token with any other number is not written (its q is).  No two tokens
  * may name one slot.  q_out_dev bf16 [tokens, heads * dim], row stride ldq_out. */
 uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
@@ -588,6 +588,72 @@ uw_status uw_cache_copy_pages(const uw_cache_config* config, int64_t layers, uin
 uw_status uw_cache_keep(const uw_cache_config* config, int64_t layers, uint16_t* k_cache_dev, uint16_t* v_cache_dev,
                         const int32_t* tables_dev, int64_t ldt, int64_t max_pages, const int32_t* starts_dev,
                         const int32_t* kept_dev, int32_t most, int64_t seqs, int32_t* lengths_dev, void* stream);
+
+/* ---- The pages of a cache, counted on the host ----
+ *
+ * Which pages of a cache are free, and how many sequences' tables hold each of the
+ * others.  Nothing here touches the device: a table's rows are copied by
+ * uw_cache_copy_pages where a call below says so.  Calls on one uw_pages must not
+ * overlap in time.  A refused call changes nothing. */
+typedef struct uw_page_counts* uw_pages;
+
+/* Pages 0 .. pages-1 (1..2^26), all free. */
+uw_status uw_pages_create(int64_t pages, uw_pages* out);
+void uw_pages_free(uw_pages p);
+int64_t uw_pages_left(uw_pages p);
+/* How many tables hold a page (0: free, or none of these pages). */
+int32_t uw_pages_holders(uw_pages p, int32_t page);
+/* The n lowest free pages in rising order, held once each (UW_ERR_OOM if fewer are
+ * left). */
+uw_status uw_pages_take(uw_pages p, int64_t n, int32_t* pages);
+/* A fork: each of n pages is held once more. */
+uw_status uw_pages_share(uw_pages p, const int32_t* pages, int64_t n);
+/* Each of n pages is held once less; one that nobody holds is free.  UW_ERR_INVALID_ARG
+ * if one is free, or named more often than it is held. */
+uw_status uw_pages_drop(uw_pages p, const int32_t* pages, int64_t n);
+/* Before a table's page is written: *own is the page itself if it is held once, else
+ * the lowest free page, which takes its place in the table (held once, the other once
+ * less): copy page to *own then. */
+uw_status uw_pages_own(uw_pages p, int32_t page, int32_t* own);
+/* Move the used pages together: *n moves from pages src[i], rising, to the lowest free
+ * pages dst[i], after which the used ones are 0 .. used-1.  src and dst have room for
+ * every page.  Copy them in one uw_cache_copy_pages call (no page is both a source and a
+ * destination) and rename them in the tables. */
+uw_status uw_pages_compact(uw_pages p, int32_t* src, int32_t* dst, int64_t* n);
+
+/* What uw_attention_forward's calls of uw_cache_write and uw_attend share, as there
+ * (device memory; axis, slopes, prefix, first and mask may be NULL). */
+typedef struct {
+  const int32_t* positions; /* [axes, tokens]     */
+  const float* freqs;       /* [pairs]            */
+  const int32_t* axis;      /* [pairs]            */
+  const int32_t* slots;     /* [tokens]           */
+  const int32_t* offsets;   /* [seqs + 1]         */
+  const int32_t* lengths;   /* [seqs]             */
+  const int32_t* tables;    /* [seqs, ldt]        */
+  const float* slopes;      /* [heads]            */
+  const int32_t* prefix;    /* [seqs]             */
+  const int32_t* first;     /* [tokens]           */
+  const uint64_t* mask;     /* [tokens, mask_words] */
+  int64_t tokens, seqs, max_tokens, max_length, ldt, max_pages;
+  int32_t mask_words;
+} uw_attention_batch;
+
+/* One attention layer on compressed projections: q, k and v of x (handles [heads *
+ * dim, hidden] and twice [kv_heads * dim, hidden]), uw_cache_write, uw_attend over
+ * bf16 outputs, and the output projection o ([hidden, heads * dim]).  pipelines[4]
+ * (q, k, v, o) are used as in uw_mlp_forward; all four handles share one main
+ * stream, on which everything runs.  Where k and v resolve to the same gemv variant on
+ * the direct palette, their products go out as one launch.  x_dev bf16 [tokens,
+ * hidden], y_dev float [tokens, hidden], 16-byte aligned; work_dev 256-byte aligned,
+ * uw_attention_workspace_bytes bytes (0 for arguments out of range).  Every argument is
+ * checked before anything is launched. */
+size_t uw_attention_workspace_bytes(const uw_cache_config* config, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                                    int64_t max_length);
+uw_status uw_attention_forward(uw_handle q, uw_handle k, uw_handle v, uw_handle o, const int32_t* pipelines,
+                               const uw_cache_config* config, const uw_rotary* rotary, const uw_attend_config* options,
+                               const uw_attention_batch* batch, const uint16_t* x_dev, uint16_t* k_cache_dev,
+                               uint16_t* v_cache_dev, float* y_dev, void* work_dev, size_t work_bytes);
 
 /* ---- Streams with a CU mask (section 九's decode/compute split) ---- */
 

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import decode_gemm_bf16_amd as uw
+import synth
 
 L = uw._lib
 INVALID, SHAPE, UNSUPPORTED = uw.ERR_INVALID_ARG, uw.ERR_SHAPE, uw.ERR_UNSUPPORTED
@@ -142,3 +143,42 @@ def test_python_refuses_tensors():
         uw.cache_copy_pages(kc, kc, i, i)
     with pytest.raises(ValueError, match="dimensions"):
         uw.cache_keep(kc, kc, pos, i, pos, i)
+
+
+def test_layer_refuses():
+    host = uw.FMT_PALETTE | uw.ENC_HOST_ONLY
+    mk = lambda r, c, s: uw.Matrix(synth.weights(r, c, s, 0.0, 0), host)  # noqa: E731
+    q, k, v, o = mk(128, 192, 1), mk(64, 192, 2), mk(64, 192, 3), mk(192, 128, 4)
+    config = cache(heads=2, kv_heads=1, dim=64, page=32, pages=10)
+    good = dict(positions=AT[3], freqs=AT[4], axis=None, slots=AT[5], offsets=AT[6], lengths=AT[7], tables=AT[8], slopes=None,
+                prefix=None, first=None, mask=None, tokens=6, seqs=2, max_tokens=3, max_length=5000, ldt=20, max_pages=20,
+                mask_words=0)
+    need = L.uw_attention_workspace_bytes(C.byref(config), 6, 2, 3, 5000)
+    assert need > 0
+
+    def call(hs=(q, k, v, o), pipelines=(4, 4, 4, 4), config=config, rotary=uw.Rotary(1, 32, 0), options=uw.AttendConfig(0.1, 0, 0),
+             x=AT[0], kc=AT[1], vc=AT[2], y=AT[9], work=AT[10], work_bytes=need, batch=True, **kw):
+        b = uw.AttentionBatch(**dict(good, **kw))
+        by = lambda p: None if p is None else C.byref(p)  # noqa: E731
+        return L.uw_attention_forward(*[h and h._h for h in hs], pipelines and (C.c_int32 * 4)(*pipelines), by(config), by(rotary),
+                                      by(options), C.byref(b) if batch else None, x, kc, vc, y, work, work_bytes)
+
+    assert call() == UNSUPPORTED  # every check passed but the one for device copies
+    for kw, status in [(dict(hs=(None, k, v, o)), INVALID), (dict(hs=(q, k, v, None)), INVALID), (dict(pipelines=None), INVALID),
+                       (dict(config=None), INVALID), (dict(batch=False), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID),
+                       (dict(work=None), INVALID), (dict(hs=(q, k, v, q)), SHAPE), (dict(hs=(k, k, v, o)), SHAPE),
+                       (dict(hs=(q, q, v, o)), SHAPE), (dict(config=cache(heads=2, kv_heads=2, dim=64)), SHAPE),
+                       (dict(tokens=0), INVALID), (dict(tokens=(1 << 20) + 1), INVALID), (dict(seqs=0), INVALID),
+                       (dict(max_tokens=7), INVALID), (dict(max_length=0), INVALID), (dict(work_bytes=need - 1), INVALID),
+                       (dict(work=AT[10] + 128), INVALID), (dict(x=AT[0] + 8), INVALID), (dict(y=AT[9] + 4), INVALID)]:
+        assert call(**kw) == status, kw
+        assert uw.last_error()
+    side = mk(64, 192, 2)
+    side.set_streams(main=0x1000)  # never used: the check fails first
+    assert call(hs=(q, side, v, o)) == INVALID and "stream" in uw.last_error()
+    for kw in (dict(tokens=0), dict(seqs=0), dict(max_tokens=0), dict(max_length=0), dict(max_tokens=7)):
+        d = dict(tokens=6, seqs=2, max_tokens=3, max_length=5000)
+        d.update(kw)
+        assert L.uw_attention_workspace_bytes(C.byref(config), *d.values()) == 0, kw
+    assert L.uw_attention_workspace_bytes(C.byref(cache(heads=3)), 6, 2, 3, 5000) == 0
+    assert L.uw_attention_workspace_bytes(None, 6, 2, 3, 5000) == 0
