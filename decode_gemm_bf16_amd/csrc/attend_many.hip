@@ -62,11 +62,13 @@ struct UnitOrder {
 // One unit of work of a wave.  S: products of kt's keys to xn.  W: x, the products of
 // block kb, become weights.  P: the weights p times vt's values; p then holds the new
 // ones.  FIRST: no operand is read yet.  NEXT: the next unit's are there, (kn, vn).
-template <int D, int MODE>
+// EDGES: block kb may hold keys that rows do not see.
+template <int D, int MODE, bool EDGES>
 struct Unit {
   using Order = UnitOrder<D>;
   const AttendArgs& a;
   const Row& r;
+  const Range& g;
   const bf16x8 (&q)[D / 16];
   const float sc;
   const int half, key_lane, value_lane;
@@ -100,6 +102,12 @@ struct Unit {
     uint32_t wt[8];
     float last = 0.f;
     if (S) xn = f32x16{};
+    if (W && EDGES && (kb < g.lo_all || kb + 32 > g.hi_all)) {
+      const int lower = r.lower - kb - 4 * half, upper = r.upper - kb - 4 * half;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (key_of(e) < lower || key_of(e) >= upper) x[e] = kNone;
+    }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kAll; ++i) {
@@ -173,12 +181,12 @@ struct Unit {
 // before it is used.  The tiles are LDS objects of their own, and page numbers scalar
 // loads, so that the compiler's waits for what is used leave the loads in flight.
 //
-// Where every row sees every key (all but the ends of most sequences) a wave works on
+// Where every row sees every key (EDGES: up to a sequence's last block) a wave works on
 // three blocks of 32 keys at once: the products of the keys of block u + 1, the softmax
 // of block u, and the products with the values of block u - 1.  The three depend on
 // nothing of each other's, and a matrix instruction (32 cycles) covers the six or so
 // vector instructions that stand beside it.
-template <int D, int MODE>
+template <int D, int MODE, bool EDGES>
 __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
   constexpr int kBytes = 64 * D;               // of a block's keys, or values
   constexpr int kSteps = D / 16;               // products of a block's keys, and of its values
@@ -215,10 +223,14 @@ __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kern
   };
   // blocks that some row of the workgroup sees, and those that every row sees all of
   const int b0 = least(0) >> 5, b1 = (31 - least(1)) >> 5;
-  const int f0 = (31 - least(2)) >> 5, f1 = least(3) >> 5;
+  int f0 = (31 - least(2)) >> 5, f1 = least(3) >> 5;
+  if (EDGES && !(a.slopes && a.prefix)) {  // (keys ahead of a row: as far off as those behind it)
+    f0 = b0;
+    f1 = (a.mask && s.start < s.keys ? s.start : s.keys) >> 5;  // (may be negative)
+  }
   const int key_lane = lane * 16, value_lane = (half * D + (lane & 31)) * 16;
   bf16x8 ring[UnitOrder<D>::kAhead];
-  const Unit<D, MODE> unit{a, r, q, sc, half, key_lane, value_lane, ring, c};
+  const Unit<D, MODE, EDGES> unit{a, r, g, q, sc, half, key_lane, value_lane, ring, c};
 
   struct Place {
     int64_t at[2];
@@ -331,11 +343,26 @@ __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kern
   put_all(a, r, z, half, c);
 }
 
+template <int D, int MODE, bool EDGES>
+void launch_edges(const AttendArgs& a, hipStream_t s) {
+  const int64_t tiles = (int64_t)a.tokens * a.group / kManyRows + a.seqs;  // at most
+  hipLaunchKernelGGL((attend_many_kernel<D, MODE, EDGES>), dim3((unsigned)(tiles * a.kv_heads), (unsigned)a.splits),
+                     dim3(64 * kWaves), 0, s, a);
+}
+
+// EDGES where many blocks are seen in part: with documents, and with short heads, whose
+// 128 rows are 128 tokens of one head as a rule (24 chunks of up to 700 tokens, heads of 64,
+// a window: 104 -> 94 us; documents of 300 tokens, heads of 128: 85 -> 74).  Elsewhere its
+// branch costs more than it saves (chunks of 4 heads of 128 a key head: 221 -> 232), and the
+// places of a cap's scores are hidden after it.
 template <int D, int MODE>
 void launch(const AttendArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)a.tokens * a.group / kManyRows + a.seqs;  // at most
-  hipLaunchKernelGGL((attend_many_kernel<D, MODE>), dim3((unsigned)(tiles * a.kv_heads), (unsigned)a.splits),
-                     dim3(64 * kWaves), 0, s, a);
+  if constexpr (MODE & kCap)
+    launch_edges<D, MODE, false>(a, s);
+  else if constexpr (D < 128)
+    launch_edges<D, MODE, true>(a, s);
+  else
+    a.first ? launch_edges<D, MODE, true>(a, s) : launch_edges<D, MODE, false>(a, s);
 }
 
 template <int D>
