@@ -128,9 +128,10 @@ void join(const AttendArgs& a, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
-// Parts of the keys: enough workgroups to fill the chip, of at least so many keys.
+// Parts of the keys: enough workgroups to fill the chip, of at least so many keys; fewer
+// where a window leaves fewer keys to see (the workspace is sized without it).
 AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
-                       int64_t max_length) {
+                       int64_t max_length, int64_t window) {
   AttendPlan p;
   const int64_t group = heads / kv_heads, per = kAttendRows;
   p.wide = max_tokens * group > 32;
@@ -141,19 +142,28 @@ AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_h
     tiles *= (max_tokens * group + per - 1) / per;
     if (tiles > most) tiles = most;
   }
-  const int64_t groups = tiles * kv_heads, blocks = (max_length + 31) / 32;
-  const int64_t want = p.wide ? 512 : 256, least = p.wide ? 16 : 8;  // workgroups; blocks of a part
-  int64_t splits = (want + groups - 1) / groups;
-  const int64_t most = blocks / least > 1 ? blocks / least : 1;
-  if (splits > most) splits = most;
-  if (!p.wide && blocks <= 48) splits = 1;
-  if (splits > 256) splits = 256;
-  int64_t chunk = (blocks + splits - 1) / splits;
-  const int64_t whole = p.wide ? 4 : kFewWaves;
-  chunk = (chunk + whole - 1) / whole * whole;
-  p.chunk = (int32_t)chunk;
-  p.splits = (int32_t)((blocks + chunk - 1) / chunk);
-  p.bytes = p.splits > 1 ? size_t(p.splits) * size_t(tokens) * heads * (dim + 2) * 4 : 0;
+  const int64_t groups = tiles * kv_heads;
+  auto divide = [&](int64_t blocks) {
+    const int64_t want = p.wide ? 512 : 256, least = p.wide ? 16 : 8;  // workgroups; blocks of a part
+    int64_t splits = (want + groups - 1) / groups;
+    const int64_t most = blocks / least > 1 ? blocks / least : 1;
+    if (splits > most) splits = most;
+    if (!p.wide && blocks <= 48) splits = 1;
+    if (splits > 256) splits = 256;
+    int64_t chunk = (blocks + splits - 1) / splits;
+    const int64_t whole = p.wide ? 4 : 8;
+    chunk = (chunk + whole - 1) / whole * whole;
+    p.chunk = (int32_t)chunk;
+    p.splits = (int32_t)((blocks + chunk - 1) / chunk);
+  };
+  const int64_t blocks = (max_length + 31) / 32, seen = window > 0 ? (window + max_tokens + 31) / 32 + 1 : blocks;
+  divide(blocks);
+  const int32_t splits = p.splits;
+  p.bytes = splits > 1 ? size_t(splits) * size_t(tokens) * heads * (dim + 2) * 4 : 0;
+  if (seen < blocks) {
+    divide(seen);
+    if (p.splits > splits) p.splits = splits;
+  }
   return p;
 }
 

@@ -28,7 +28,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -INFINITY;
 constexpr int kWaves = 4;     // of a workgroup with many rows
-constexpr int kFewWaves = 8;  // with few
+constexpr int few_waves(int dim) { return dim > 128 ? 4 : 8; }  // with few
 // A row's maximum moves only when a score is this far above it (in powers of two):
 // weights stay below 2^8, and most blocks leave the sums as they are.
 constexpr float kSlack = 8.f;

@@ -27,10 +27,11 @@ __device__ __forceinline__ float sum_of_row(float v) {
 // of 32 keys; the keys of the next block are on their way during the softmax, its
 // values during the next product.
 template <int D, int MODE, int R>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
+  constexpr int kAcross = few_waves(D);
   constexpr int kTiles = D / 16, kRound = kTiles < 8 ? kTiles : 8;  // of 16 elements; joined at once
-  __shared__ __attribute__((aligned(16))) f32x4 join[kFewWaves][kRound][64];
-  __shared__ float share[2][kFewWaves][16];
+  __shared__ __attribute__((aligned(16))) f32x4 join[kAcross][kRound][64];
+  __shared__ float share[2][kAcross][16];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   const int kvh = blockIdx.x, z = blockIdx.z;
   const int lane_key = 16 * (grp >> 1) + 4 * (grp & 1);
@@ -89,9 +90,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(AttendArg
       int64_t at = where(p0 + w, bad);
       load_k(at, bad);
       load_v(at, bad);
-      for (int blk = p0 + w; blk < p1; blk += kFewWaves) {
+      for (int blk = p0 + w; blk < p1; blk += kAcross) {
         bool next_bad;
-        const int64_t next = where(blk + kFewWaves, next_bad);
+        const int64_t next = where(blk + kAcross, next_bad);
         const int kb = blk << 5;
         float x[R][8];
         f32x4 product[R][2] = {};
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(AttendArg
       again = true;
       goto from_the_start;
     }
-    for (int blk = odd.first; blk <= odd.last; blk += kFewWaves) {  // what was held back, to the rows that see it
+    for (int blk = odd.first; blk <= odd.last; blk += kAcross) {  // what was held back, to the rows that see it
       int64_t at;
       if (!block_at(a, s, kvh, blk, D, at)) continue;
 #pragma unroll
@@ -209,10 +210,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(AttendArg
       __syncthreads();
       float all = kNone, weight = 0.f;
 #pragma unroll
-      for (int i = 0; i < kFewWaves; ++i) all = __builtin_fmaxf(all, share[0][i][col]);
+      for (int i = 0; i < kAcross; ++i) all = __builtin_fmaxf(all, share[0][i][col]);
       const float ref = all == kNone ? 0.f : all;
 #pragma unroll
-      for (int i = 0; i < kFewWaves; ++i) {
+      for (int i = 0; i < kAcross; ++i) {
         const float e = share[1][i][col];
         weight += e == 0.f ? 0.f : e * __builtin_amdgcn_exp2f(share[0][i][col] - ref);
       }
@@ -225,11 +226,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(AttendArg
           if (t0 + t < kTiles && r[n].live) join[w][t][lane] = o[n * kTiles + t0 + t] * f;
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < kRound; t += kFewWaves)
+        for (int t = 0; t < kRound; t += kAcross)
           if (t + w < kRound && t0 + t + w < kTiles && r[n].live) {
             f32x4 sum = join[0][t + w][lane];
 #pragma unroll
-            for (int k = 1; k < kFewWaves; ++k) sum += join[k][t + w][lane];
+            for (int k = 1; k < kAcross; ++k) sum += join[k][t + w][lane];
             put(a, r[n], z, (t0 + t + w) * 16 + 4 * grp, sum, weight);
           }
       }
@@ -243,9 +244,9 @@ template <int D, int MODE>
 void launch(const AttendArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.kv_heads, (unsigned)a.seqs, (unsigned)a.splits);
   if (a.rows <= 16)
-    hipLaunchKernelGGL((attend_few_kernel<D, MODE, 1>), grid, dim3(64 * kFewWaves), 0, s, a);
+    hipLaunchKernelGGL((attend_few_kernel<D, MODE, 1>), grid, dim3(64 * few_waves(D)), 0, s, a);
   else
-    hipLaunchKernelGGL((attend_few_kernel<D, MODE, 2>), grid, dim3(64 * kFewWaves), 0, s, a);
+    hipLaunchKernelGGL((attend_few_kernel<D, MODE, 2>), grid, dim3(64 * few_waves(D)), 0, s, a);
 }
 
 template <int D>

@@ -217,7 +217,7 @@ uw_status attend_prepare(const uw_cache_config* config, const uw_attend_config* 
       !aligned(prefix_dev, 4) || !aligned(first_dev, 4) || !aligned(mask_dev, 8) || !aligned(lse_dev, 4))
     return fail(UW_ERR_INVALID_ARG, "misaligned pointer");
   AttendPlan& plan = *plan_out;
-  plan = attend_plan(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length);
+  plan = attend_plan(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length, prefix_dev ? 0 : options->window);
   if (plan.bytes && (!work_dev || work_bytes < plan.bytes))
     return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, the call needs %zu", work_dev ? work_bytes : size_t(0), plan.bytes);
   if (plan.bytes && !aligned(work_dev, 16)) return fail(UW_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");

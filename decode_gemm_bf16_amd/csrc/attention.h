@@ -85,7 +85,7 @@ struct AttendPlan {
   size_t bytes;  // of the workspace
 };
 AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
-                       int64_t max_length);
+                       int64_t max_length, int64_t window = 0);
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t s);
 hipError_t launch_attend_few(const AttendArgs& a, hipStream_t s);   // (with its parts set)
 hipError_t launch_attend_many(const AttendArgs& a, hipStream_t s);
