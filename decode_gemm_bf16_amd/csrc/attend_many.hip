@@ -168,7 +168,12 @@ struct Unit {
       p[1] = as_bf16x8(wt[4], wt[5], wt[6], wt[7]);
       if (moved) {
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t) c.o[t] *= f;
+        for (int t = 0; t < D / 32; ++t) {
+          // (the sums of long heads fill the accumulators' half of the registers and stay there)
+          if (D > 128) asm volatile("" : "+a"(c.o[t]));
+          c.o[t] *= f;
+          if (D > 128) asm volatile("" : "+a"(c.o[t]));
+        }
       }
     }
   }
