@@ -126,44 +126,55 @@ void join(const AttendArgs& a, dim3 grid, hipStream_t s) {
   hipLaunchKernelGGL((attend_join_kernel<ONE, H>), grid, dim3(256), 0, s, a);
 }
 
-}  // namespace
-
-// Parts of the keys: enough workgroups to fill the chip, of at least so many keys; fewer
-// where a window leaves fewer keys to see (the workspace is sized without it).
-AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
-                       int64_t max_length, int64_t window) {
+// The plan for sequences of so many blocks of 32 keys.
+//
+// Few rows a sequence, up to 32, take the kernel that streams keys past them.  So do more
+// of them where the whole call is up to 256 workgroups of 32 rows and the keys are short:
+// eight waves divide a workgroup's keys there, which takes less time from the first key to
+// the last than 128 rows that walk them all (one sequence of 24 tokens, 32 heads of 128 on 8:
+// 200 keys 19.5 -> 14.4 us, 600 19.4 -> 13.4; 61 tokens, 6000 keys 32.5 -> 29.1; but 30000
+// keys 44 -> 73, and 24 keys 9.5 -> 11).  Heads of 256 turn earlier (2000 keys 61 -> 66).
+//
+// Parts of the keys: enough workgroups to fill the chip, two a unit of the kernel for many
+// rows and one of the other, of at least so many keys that joining them is worth it.
+AttendPlan plan_for(int64_t tokens, int64_t seqs, int64_t group, int64_t kv_heads, int64_t dim, int64_t max_tokens,
+                    int64_t blocks) {
   AttendPlan p;
-  const int64_t group = heads / kv_heads, per = kAttendRows;
-  p.wide = max_tokens * group > 32;
-  p.rows = (int32_t)(max_tokens * group);
-  int64_t tiles = seqs;
+  const int64_t rows = max_tokens * group;
+  p.rows = (int32_t)rows;
+  int64_t tiles = seqs * ((rows + 31) / 32);
+  const bool short_keys = blocks >= 4 && blocks <= (dim > 128 ? 48 : 192);
+  p.wide = rows > 32 && !(short_keys && tiles * kv_heads <= 256);
   if (p.wide) {
-    const int64_t most = tokens * group / per + seqs;
-    tiles *= (max_tokens * group + per - 1) / per;
+    const int64_t most = tokens * group / kAttendRows + seqs;
+    tiles = seqs * ((rows + kAttendRows - 1) / kAttendRows);
     if (tiles > most) tiles = most;
   }
-  const int64_t groups = tiles * kv_heads;
-  auto divide = [&](int64_t blocks) {
-    const int64_t want = p.wide ? 512 : 256, least = p.wide ? 16 : 8;  // workgroups; blocks of a part
-    int64_t splits = (want + groups - 1) / groups;
-    const int64_t most = blocks / least > 1 ? blocks / least : 1;
-    if (splits > most) splits = most;
-    if (!p.wide && blocks <= 48) splits = 1;
-    if (splits > 256) splits = 256;
-    int64_t chunk = (blocks + splits - 1) / splits;
-    const int64_t whole = p.wide ? 4 : 8;
-    chunk = (chunk + whole - 1) / whole * whole;
-    p.chunk = (int32_t)chunk;
-    p.splits = (int32_t)((blocks + chunk - 1) / chunk);
-  };
-  const int64_t blocks = (max_length + 31) / 32, seen = window > 0 ? (window + max_tokens + 31) / 32 + 1 : blocks;
-  divide(blocks);
-  const int32_t splits = p.splits;
-  p.bytes = splits > 1 ? size_t(splits) * size_t(tokens) * heads * (dim + 2) * 4 : 0;
-  if (seen < blocks) {
-    divide(seen);
-    if (p.splits > splits) p.splits = splits;
-  }
+  const int64_t groups = tiles * kv_heads, want = p.wide ? 512 : 256, least = p.wide ? 16 : 8, whole = p.wide ? 4 : 8;
+  int64_t splits = (want + groups - 1) / groups;
+  const int64_t most = blocks / least > 1 ? blocks / least : 1;
+  if (splits > most) splits = most;
+  if (!p.wide && blocks <= 48) splits = 1;
+  if (splits > 256) splits = 256;
+  int64_t chunk = (blocks + splits - 1) / splits;
+  chunk = (chunk + whole - 1) / whole * whole;
+  p.chunk = (int32_t)chunk;
+  p.splits = (int32_t)((blocks + chunk - 1) / chunk);
+  p.bytes = p.splits > 1 ? size_t(p.splits) * size_t(tokens) * kv_heads * group * (dim + 2) * 4 : 0;
+  return p;
+}
+
+}  // namespace
+
+// A window leaves fewer keys to see, and so fewer parts; the workspace is sized without it.
+AttendPlan attend_plan(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_tokens,
+                       int64_t max_length, int64_t window) {
+  const int64_t blocks = (max_length + 31) / 32, seen = (window + max_tokens + 31) / 32 + 1;
+  const AttendPlan all = plan_for(tokens, seqs, heads / kv_heads, kv_heads, dim, max_tokens, blocks);
+  if (window <= 0 || seen >= blocks) return all;
+  AttendPlan p = plan_for(tokens, seqs, heads / kv_heads, kv_heads, dim, max_tokens, seen);
+  if (p.splits > all.splits) p.splits = all.splits;
+  p.bytes = all.bytes;
   return p;
 }
 

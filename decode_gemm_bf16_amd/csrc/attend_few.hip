@@ -33,11 +33,12 @@ __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few
   __shared__ __attribute__((aligned(16))) f32x4 join[kAcross][kRound][64];
   __shared__ float share[2][kAcross][16];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
-  const int kvh = blockIdx.x, z = blockIdx.z;
+  const int kvh = (int)blockIdx.x % a.kv_heads, z = blockIdx.z;
+  const int row0 = (int)blockIdx.x / a.kv_heads * 16 * R, row_step = (int)gridDim.x / a.kv_heads * 16 * R;
   const int lane_key = 16 * (grp >> 1) + 4 * (grp & 1);
   const Seq s = sequence(a, blockIdx.y);
   const float sc = MODE ? 1.f : a.scale * kLog2e;
-  for (int r0 = 0; r0 < s.count * a.group; r0 += 16 * R) {
+  for (int r0 = row0; r0 < s.count * a.group; r0 += row_step) {
     Row r[R];
     bf16x8 q[R][D / 32];
 #pragma unroll
@@ -242,8 +243,9 @@ __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few
 
 template <int D, int MODE>
 void launch(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.kv_heads, (unsigned)a.seqs, (unsigned)a.splits);
-  if (a.rows <= 16)
+  const int each = a.rows <= 16 ? 16 : 32;
+  const dim3 grid((unsigned)(a.kv_heads * ((a.rows + each - 1) / each)), (unsigned)a.seqs, (unsigned)a.splits);
+  if (each == 16)
     hipLaunchKernelGGL((attend_few_kernel<D, MODE, 1>), grid, dim3(64 * few_waves(D)), 0, s, a);
   else
     hipLaunchKernelGGL((attend_few_kernel<D, MODE, 2>), grid, dim3(64 * few_waves(D)), 0, s, a);

@@ -182,3 +182,17 @@ def test_layer_refuses():
         assert L.uw_attention_workspace_bytes(C.byref(config), *d.values()) == 0, kw
     assert L.uw_attention_workspace_bytes(C.byref(cache(heads=3)), 6, 2, 3, 5000) == 0
     assert L.uw_attention_workspace_bytes(None, 6, 2, 3, 5000) == 0
+
+
+def test_a_window_asks_for_no_more_workspace():
+    """The workspace is sized without the window that the call has."""
+    for heads, kv, dim in ((8, 2, 64), (32, 8, 128), (4, 1, 256)):
+        for tokens, seqs in ((1, 1), (24, 1), (61, 4), (700, 3)):
+            for length in (100, 3000, 40000, 200000):
+                need = uw.attend_workspace_bytes(tokens * seqs, seqs, heads, kv, dim, tokens, length)
+                for window in (0, 1, 500, 3000, 30000, 2 ** 31 - 1):
+                    # (refused for its tables, the last of the checks before the workspace's that can be)
+                    good = dict(config=cache(heads=heads, kv_heads=kv, dim=dim), ldq=heads * dim, ldy=heads * dim, window=window,
+                                tokens=tokens * seqs, seqs=seqs, max_tokens=tokens, max_length=length, lse=AT[5])
+                    assert attend(work=AT[8] if need else None, work_bytes=need, **good) == INVALID
+                    assert "overlap" in uw.last_error(), (heads, tokens, seqs, length, window, uw.last_error())
