@@ -1,4 +1,4 @@
-// Attention with few rows a sequence: single tokens and short runs of them.
+// Attention with few rows: single tokens, short runs of them, small calls.
 #include "attend_core.h"
 
 namespace uw {
@@ -25,7 +25,14 @@ __device__ __forceinline__ float sum_of_row(float v) {
 // Bound by HBM: each key and value is read once, from memory straight into the
 // registers of the products (lines of 128 bytes whole).  A wave takes every eighth block
 // of 32 keys; the keys of the next block are on their way during the softmax, its
-// values during the next product.
+// values during the next product.  64 sequences of up to 8192 keys, 32 heads of 128 on 8:
+// 192 us (5.8 TB/s; with four waves 216, with cached loads 262 against 234); two of 131072
+// 161 us (6.5 TB/s; four waves 184).  Heads of 256 fill 512 registers and have four waves
+// (32 sequences of 8192 keys 315 us, 6.8 TB/s, against 366 with eight; two tiles of rows 190
+// against 479).
+//
+// A workgroup has up to 32 rows of a sequence and key head (R = 2; up to 16 one tile of
+// them), others the next ones; keys are read again for those, out of the L2.
 template <int D, int MODE, int R>
 __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
   constexpr int kAcross = few_waves(D);

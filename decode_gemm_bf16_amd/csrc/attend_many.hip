@@ -189,8 +189,16 @@ struct Unit {
 // Where every row sees every key (EDGES: up to a sequence's last block) a wave works on
 // three blocks of 32 keys at once: the products of the keys of block u + 1, the softmax
 // of block u, and the products with the values of block u - 1.  The three depend on
-// nothing of each other's, and a matrix instruction (32 cycles) covers the six or so
-// vector instructions that stand beside it.
+// nothing of each other's, and the vector instructions of one hide, with two waves a SIMD,
+// behind half of the matrix instructions of the others (8 products of 32x32x16 131 ns, 96
+// FMA 110, both 187).  That bounds it: a prompt of 8192 tokens, 32 heads of 128 on 8, 521 us
+// (1.05 PFLOP/s; the library's matrix product reaches 1.2); with a cap, whose tanh is five
+// more instructions a score, trees of 61 tokens over 6144 keys 0.57 PFLOP/s.  64 rows a
+// wave, which read LDS half as often, leave one wave a SIMD, and that issues vector
+// instructions at half the rate (722 us against 613, under a profiler).
+//
+// Heads of 256 have one wave a SIMD all the same: their sums take half of its registers
+// (prompt of 4096 tokens 410 us, 0.67 PFLOP/s).
 template <int D, int MODE, bool EDGES>
 __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
   constexpr int kBytes = 64 * D;               // of a block's keys, or values
