@@ -118,6 +118,7 @@ __device__ __forceinline__ Row row_of(const AttendArgs& a, const Seq& s, int kvh
   o.lower = a.window > 0 && o.pos - a.window + 1 > 0 ? o.pos - a.window + 1 : 0;
   o.first = a.first ? a.first[o.token] : 0;
   if (o.first > o.lower) o.lower = o.first;
+  if (o.lower > s.keys) o.lower = s.keys;  // (a mark may be any number; sums with this one stay small)
   o.slope = a.slopes ? a.slopes[o.head] * kLog2e : 0.f;
   return o;
 }
