@@ -15,6 +15,8 @@
 // maxima, sums, and outputs until their end are float32.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.h"
 #include "recon.h"
 
@@ -199,16 +201,59 @@ __device__ __forceinline__ void clear(Sums<D>& c) {
   c.l = 0.f;
 }
 
-// What a kernel is built for: a cap, slopes, both or neither.
-constexpr int kCap = 1, kSlopes = 2;
+// What a kernel is built for: a cap (a far one, too), slopes, both or neither.
+constexpr int kCap = 1, kSlopes = 2, kFar = 4;
+template <typename F>  // f(the kernel's)
+inline void with_mode(const AttendArgs& a, F f) {
+  const bool far = a.cap > kNearCap;
+  if (a.slopes)
+    far ? f(std::integral_constant<int, kCap | kSlopes | kFar>{})
+        : a.cap > 0.f ? f(std::integral_constant<int, kCap | kSlopes>{}) : f(std::integral_constant<int, kSlopes>{});
+  else
+    far ? f(std::integral_constant<int, kCap | kFar>{})
+        : a.cap > 0.f ? f(std::integral_constant<int, kCap>{}) : f(std::integral_constant<int, 0>{});
+}
 
-// cap tanh of a product, in powers of two.
+// cap tanh(scale x / cap) of a product x, in powers of two.  tanh u = 1 - 2 / (1 + e^2u) is off
+// by up to 4 * 2^-23 of the cap, whatever the score, with exponential and reciprocal within a
+// step each: right for caps near the scores, but all of a score of 8 at 1e8.
 struct Cap {
   float in, out;
-  __device__ __forceinline__ explicit Cap(const AttendArgs& a)
-      : in(a.scale / a.cap * (2.f * kLog2e)), out(a.cap * kLog2e) {}
+  __device__ __forceinline__ explicit Cap(const AttendArgs& a) : in(a.cap_in), out(a.cap_out) {}
   __device__ __forceinline__ float operator()(float x) const {
     return __builtin_fmaf(-2.f * out, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * in)), out);
+  }
+};
+
+// The same for caps further off (kFar): up to u = scale x / cap = 1/2, as hardly any score
+// passes, it is scale x times a polynomial in u^2, fitted to tanh(u) / u - 1 within 0.3 * 2^-24,
+// so that its error is relative to the score; from there on the other form's is, too, 8 * 2^-23
+// of it at most.  A prompt of 8192 tokens 703 us, with the other form 668; where scores do pass
+// 1/2 it costs more (trees of 61 tokens over 6000 keys at a cap of 8 234 against 171, prompts of
+// 4096 tokens with heads of 256 at 50 416 against 393), so near caps keep theirs.
+struct FarCap {
+  float in, scale;
+  __device__ __forceinline__ explicit FarCap(const AttendArgs& a)
+      : in(a.cap_in * (0.5f * kLn2)), scale(a.scale * kLog2e) {}
+  // What is capped already stays as it is.
+  __device__ __forceinline__ void pass() { in = 0.f, scale = 1.f; }
+  __device__ __forceinline__ float operator()(float x, float more) const {  // up to 1/2; and `more`
+    const float u = x * in, z = u * u;
+    float p = __builtin_fmaf(z, 0.01725699f, -0.05305295f);
+    p = __builtin_fmaf(z, p, 0.13325988f);
+    p = __builtin_fmaf(z, p, -0.3333315f);
+    return __builtin_fmaf(x * scale, __builtin_fmaf(z, p, 1.f), more);
+  }
+  __device__ __forceinline__ float any(const Cap& cap, float x) const {
+    return __builtin_fabsf(x * in) <= 0.5f ? (*this)(x, 0.f) : cap(x);
+  }
+  // Whether some product of a block passes 1/2.
+  template <int N, typename X>
+  __device__ __forceinline__ bool passed(const X& x) const {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) most = __builtin_fmaxf(most, __builtin_fabsf(x[i]));
+    return __ballot(most * in > 0.5f) != 0;
   }
 };
 
@@ -220,8 +265,9 @@ __device__ __forceinline__ void scores(const AttendArgs& a, const Seq& s, const 
   const int k0 = kb + lane_key;
   if (MODE & kCap) {
     const Cap cap(a);
+    const FarCap far(a);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = cap(x[i]);
+    for (int i = 0; i < N; ++i) x[i] = MODE & kFar ? far.any(cap, x[i]) : cap(x[i]);
   }
   if (MODE & kSlopes) {
     const float sc = MODE & kCap ? 1.f : a.scale * kLog2e;

@@ -260,8 +260,7 @@ void launch(const AttendArgs& a, hipStream_t s) {
 
 template <int D>
 void launch_mode(const AttendArgs& a, hipStream_t s) {
-  const int mode = (a.cap > 0.f ? kCap : 0) | (a.slopes ? kSlopes : 0);
-  mode == 0 ? launch<D, 0>(a, s) : mode == 1 ? launch<D, 1>(a, s) : mode == 2 ? launch<D, 2>(a, s) : launch<D, 3>(a, s);
+  with_mode(a, [&](auto mode) { launch<D, mode.value>(a, s); });
 }
 
 }  // namespace

@@ -95,6 +95,12 @@ struct Unit {
         if (there<S, P>(i)) ring[i] = operand(i, kt, vt);
     }
     const Cap cap(a);
+    FarCap far(a);
+    if (W && (MODE & kFar) && far.passed<16>(x)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = far.any(cap, x[e]);
+      far.pass();
+    }
     const float base = MODE & kSlopes ? -r.slope * (float)(r.pos - kb - 4 * half) : 0.f;
     float top = kNone, m = 0.f;
     bool moved = false;
@@ -130,14 +136,16 @@ struct Unit {
 #pragma unroll
           for (int e = 16 * i / kLead; e < 16 * (i + 1) / kLead; ++e) {
             if (MODE == (kCap | kSlopes)) x[e] = cap(x[e]);
-            if (MODE & kSlopes)
-              x[e] = __builtin_fmaf(x[e], MODE & kCap ? 1.f : a.scale * kLog2e,
-                                    __builtin_fmaf(r.slope, (float)key_of(e), base));
+            if (MODE & kSlopes) {
+              const float slope = __builtin_fmaf(r.slope, (float)key_of(e), base);
+              x[e] = MODE & kFar ? far(x[e], slope) : __builtin_fmaf(x[e], MODE & kCap ? 1.f : a.scale * kLog2e, slope);
+            }
             top = __builtin_fmaxf(top, x[e]);
           }
           if (i == kLead - 1) {
             top = larger_half(top);
             if (MODE == kCap) top = cap(top);
+            if (MODE == (kCap | kFar)) top = far(top, 0.f);
             if (MODE == 0) top *= sc;
             moved = __ballot(top > c.m + kSlack) != 0;
             const float was = c.m;
@@ -150,7 +158,9 @@ struct Unit {
           constexpr int kRest = kAll - kLead;
 #pragma unroll
           for (int e = 16 * (i - kLead) / kRest; e < 16 * (i - kLead + 1) / kRest; ++e) {
-            const float y = MODE == 0 ? __builtin_fmaf(x[e], sc, -m) : (MODE == kCap ? cap(x[e]) : x[e]) - m;
+            const float y = MODE == 0                ? __builtin_fmaf(x[e], sc, -m)
+                            : MODE == (kCap | kFar) ? far(x[e], -m)
+                                                    : (MODE == kCap ? cap(x[e]) : x[e]) - m;
             const float now = __builtin_amdgcn_exp2f(y);
             if (e % 2) {
               c.l += last + now;
@@ -380,8 +390,7 @@ void launch(const AttendArgs& a, hipStream_t s) {
 
 template <int D>
 void launch_mode(const AttendArgs& a, hipStream_t s) {
-  const int mode = (a.cap > 0.f ? kCap : 0) | (a.slopes ? kSlopes : 0);
-  mode == 0 ? launch<D, 0>(a, s) : mode == 1 ? launch<D, 1>(a, s) : mode == 2 ? launch<D, 2>(a, s) : launch<D, 3>(a, s);
+  with_mode(a, [&](auto mode) { launch<D, mode.value>(a, s); });
 }
 
 }  // namespace

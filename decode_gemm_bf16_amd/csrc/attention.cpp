@@ -4,9 +4,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <limits>
 
 #include "../../include/uw.h"
 #include "runtime_internal.h"
@@ -265,6 +267,10 @@ uw_status attend_prepare(const uw_cache_config* config, const uw_attend_config* 
   a.window = options->window < (1 << 30) ? options->window : 0;  // (no two places are further apart)
   a.scale = options->scale;
   a.cap = options->cap;
+  // (kept finite, so that a product of zero stays zero and a cap less itself is zero)
+  const double log2e = 1.4426950408889634, most = std::numeric_limits<float>::max();
+  a.cap_in = a.cap > 0.f ? float(std::min(double(a.scale) / a.cap * 2 * log2e, most)) : 0.f;
+  a.cap_out = float(std::min(a.cap * log2e, most / 2));
   a.y_bf16 = y_type == UW_BF16;
   return UW_OK;
 }

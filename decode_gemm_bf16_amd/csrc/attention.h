@@ -57,6 +57,10 @@ struct CacheKeepArgs {
 };
 hipError_t launch_cache_keep(const CacheKeepArgs& a, hipStream_t s);
 
+// Caps up to here take the form of tanh that is off by 4 * 2^-23 of the cap: 6e-5 of a weight at
+// 128, a 64th of its rounding to bf16.
+constexpr float kNearCap = 128.f;
+
 struct AttendArgs {
   const uint16_t* q;
   const uint16_t *kc, *vc;
@@ -74,6 +78,7 @@ struct AttendArgs {
   int32_t splits;  // parts of the keys
   int32_t chunk;   // blocks of 32 keys a part
   float scale, cap;
+  float cap_in, cap_out;  // 2 scale / cap and the cap, both in powers of two, and finite
   bool y_bf16;
 };
 // Rows of a workgroup of the kernel for many rows.

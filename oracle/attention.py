@@ -81,8 +81,9 @@ def attend(q, keys, values, count, length, scale, cap=0.0, window=0, slopes=None
     of keys: no page).  Returns y, lse and how far float32 results may be off each.
 
     With u a float32 step, a product of dim terms is off by at most dim u |q||k|, a
-    score's further steps by 8 u of their own magnitudes (a tanh's two by those of the
-    cap), so that a weight is off by the factor 1 + 2 e, e = the score's error + 4 u.
+    score's further steps by 8 u of their own magnitudes (a capped one's, too, by 8 u of
+    the smaller of score and cap, and 4 u of a cap up to 128), so that a weight is off by
+    the factor 1 + 2 e, e = the score's error + 4 u.
     Weights are rounded to bf16 (2^-8) before the product with the values, their sum is
     not; sums of n terms are off by n u.  y is rounded once (y_half)."""
     heads, kv = q.shape[1], keys.shape[1]
@@ -99,8 +100,8 @@ def attend(q, keys, values, count, length, scale, cap=0.0, window=0, slopes=None
             x = scale * (k @ q[i, h])
             e = q.shape[2] * U * scale * (np.abs(k) @ np.abs(q[i, h])) + 8 * U * np.abs(x)
             if cap:
+                e += 8 * U * np.minimum(cap, np.abs(x)) + (4 * U * cap if cap <= 128 else 0)
                 x = cap * np.tanh(x / cap)
-                e += 8 * U * cap
             if slopes is not None:
                 x = x - slopes[h] * np.abs(far)
                 e += 8 * U * np.abs(slopes[h] * far) + 8 * U * np.abs(x)

@@ -1,11 +1,11 @@
-"""Attention at the ends of its arguments' ranges (GPU): marks that hide everything;
-each laid out so that the kernel for few rows, the one for many with one part of the keys and
-with many take it."""
+"""Attention at the ends of its arguments' ranges (GPU): marks that hide everything, caps far
+above and far below the scores; each laid out so that the kernel for few rows, the one for
+many with one part of the keys and with many take it."""
 import numpy as np
 import pytest
 
 import test_gpu_attention as cases
-from test_gpu_attention import env  # noqa: F401
+from test_gpu_attention import Cache, bf16, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,13 @@ def laid_out(how, count, length, heads, kv):
     return [count] + [0] * empty, [length] + [0] * empty, dict(max_length=30000)
 
 
+def one_long(rng, lengths, kv, dim, page):
+    """A cache for the first sequence; the others, empty, have no pages."""
+    c = Cache(rng, lengths[:1], kv, dim, page)
+    c.tables = np.concatenate([c.tables, np.full((len(lengths) - 1, c.tables.shape[1]), -1, dtype=np.int32)])
+    return c
+
+
 @pytest.mark.parametrize("how", LAID_OUT)
 @pytest.mark.parametrize("dim", [64, 96, 128, 256])
 @pytest.mark.parametrize("kw", [dict(cap=20.0), dict(), dict(cap=20.0, slopes=[0.5, 0.25, 0.1, 0.0]), dict(cap=20.0, window=150)])
@@ -40,6 +47,22 @@ def test_documents_and_marks_behind_the_keys(env, how, dim, kw, mark):  # noqa: 
     counts, lengths, sizes = laid_out(how, count, length, 4, 1)
     first = [i * 37 % 300 for i in range(count)]
     first[45] = first[80] = mark
-    y, lse = cases.run(env, rng, counts, lengths, 4, 1, dim, 32, first=first, **kw, **sizes)
+    y, lse = cases.run(env, rng, counts, lengths, 4, 1, dim, 32, first=first,
+                       cache=one_long(rng, lengths, 1, dim, 32), **kw, **sizes)
     for i in (45, 80):
         assert (y[i] == 0).all() and (lse[i] == -np.inf).all()
+
+
+@pytest.mark.parametrize("how", LAID_OUT)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cap", [1e-45, 1e-38, 1.0, 128.0, 129.0, 1e4, 1e8, 3e38])
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=[0.5, 0.02, 0.1, 0.0]), dict(scale=3.0)])
+def test_caps(env, how, dim, cap, kw):  # noqa: F811
+    """Far above the scores a cap leaves them as they are, far below it leaves nothing of them."""
+    rng = np.random.default_rng(dim + 1)
+    counts, lengths, sizes = laid_out(how, 20, 260, 4, 1)
+    q = bf16(rng, 21, 4 * dim)
+    for a in q:
+        a[7] = 0  # (scores of zero)
+    cases.run(env, rng, counts, lengths, 4, 1, dim, 32, cache=one_long(rng, lengths, 1, dim, 32), q=q, cap=cap, out="f32",
+              **kw, **sizes)
