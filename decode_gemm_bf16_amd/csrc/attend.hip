@@ -45,18 +45,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = __builtin_fmaxf(m, tops[k]);
     }
-    f = e.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(e.x - (m == kNone ? 0.f : m));
-    weight = sum32(e.y * f);
-    // a part without weight has written no sums
-    const bool there = e.y != 0.f;
+    // a part's share; one without weight has written nothing (-1)
+    f = e.y == 0.f ? 0.f : e.y * __builtin_amdgcn_exp2f(e.x - (m == kNone ? 0.f : m));
+    weight = sum32(f);
+    if (e.y == 0.f) f = -1.f;
     if (ONE) {
-      factor[mine] = there ? f : -1.f;
+      factor[mine] = f;
       if (l == 0) weights[grp] = weight;
       __syncthreads();
       weight = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) weight += weights[k];
     }
+    const float inv = weight == 0.f ? 0.f : 1.f / weight;
     f32x4 o[H] = {};
     const float* const part = a.part + row * a.dim;
     const int step = ONE ? 8 : 1;
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
           if (ONE)
             g[k] = z < a.splits ? factor[z] : -1.f;
           else
-            g[k] = __shfl(there ? f : -1.f, (threadIdx.x & 32) + (z < 32 ? z : 31), 64);
+            g[k] = __shfl(f, (threadIdx.x & 32) + (z < 32 ? z : 31), 64);
           if (z >= a.splits) g[k] = -1.f;
 #pragma unroll
           for (int i = 0; i < H; ++i) {
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         for (int k = 0; k < kJoinAtOnce; ++k)
 #pragma unroll
           for (int i = 0; i < H; ++i)
-            if (!(g[k] < 0.f)) o[i] += g[k] * v[k][i];
+            if (!(g[k] < 0.f)) o[i] += g[k] * inv * v[k][i];
       }
     }
     if (ONE) {
@@ -103,12 +104,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
       }
     }
     if (live && (!ONE || grp == 0)) {
-      const float inv = weight == 0.f ? 0.f : 1.f / weight;
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const int d = i * 128 + l * 4;
         if (d >= a.dim) continue;
-        const f32x4 v = weight == 0.f ? f32x4{} : o[i] * inv;
+        const f32x4 v = o[i];
         const int64_t at = (int64_t)t * a.ldy + h * a.dim + d;
         if (a.y_bf16)
           *(u32x2*)((uint16_t*)a.y + at) = u32x2{pack(v.x, v.y), pack(v.z, v.w)};

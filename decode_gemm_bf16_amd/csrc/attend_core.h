@@ -34,6 +34,10 @@ constexpr int few_waves(int dim) { return dim > 128 ? 4 : 8; }  // with few
 // A row's maximum moves only when a score is this far above it (in powers of two):
 // weights stay below 2^8, and most blocks leave the sums as they are.
 constexpr float kSlack = 8.f;
+// Sums that are not finite are done again with the weights of the second product times
+// kLess: of 2^30 values below 2^128 none is infinite then.  (A power of two: the sums' bits stay
+// as they are.)  kMore undoes it.
+constexpr float kLess = 0x1p-40f, kMore = 0x1p40f;
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
@@ -311,7 +315,8 @@ __device__ __forceinline__ void scores(const AttendArgs& a, const Seq& s, const 
 // sequence's end may hold anything) and take the others as they are; where a sum is not
 // finite then, the rows are done again by careful() below: it sets infinities and NaN to
 // zero in blocks that some rows see in part, remembers these blocks and adds what it held
-// back to the rows that see it.
+// back to the rows that see it.  The sums of finite values that are large stay finite there;
+// whoever adds up sums of several waves or parts normalises them first.
 __device__ __forceinline__ u32x4 tame(u32x4 v, const u32x4& keep, uint32_t& odd) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -357,8 +362,8 @@ struct Odd {
 };
 
 // A block of 32 keys from kb on: x holds their products with the lane's query.  ALL:
-// every row sees all of them.  TAME: infinities and NaN are held back.  hidden: the
-// block has no page.
+// every row sees all of them.  TAME: infinities and NaN are held back, weights are times
+// kLess.  hidden: the block has no page.
 template <int D, int MODE, bool ALL, bool TAME, typename V>
 __device__ __forceinline__ void take(const AttendArgs& a, const Seq& s, const Row& r, const Range& g, float sc, int kb,
                                      int half, f32x16& x, bool hidden, Sums<D>& c, Odd& odd, const V& value) {
@@ -386,7 +391,7 @@ __device__ __forceinline__ void take(const AttendArgs& a, const Seq& s, const Ro
     const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], sc, -m));
     const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 1], sc, -m));
     c.l += p0 + p1;
-    w[i / 2] = pack(p0, p1);
+    w[i / 2] = TAME ? pack(p0 * kLess, p1 * kLess) : pack(p0, p1);
   }
   const bf16x8 p[2] = {as_bf16x8(w[0], w[1], w[2], w[3]), as_bf16x8(w[4], w[5], w[6], w[7])};
   const int lo = hidden ? 1 << 30 : g.lo;
@@ -487,16 +492,15 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Row& r, in
   for (int t = 0; t < D / 16; ++t) q[t] = *(const bf16x8*)(p + 16 * t);
 }
 
-// Four sums of a row (elements d .. d + 3): to y where the keys are not split, else to
-// the part's place.
+// Four elements (d .. d + 3) of a row, normalised: to y where the keys are not split, else
+// to the part's place.
 __device__ __forceinline__ void put(const AttendArgs& a, const Row& r, int z, int d, f32x4 o, float weight) {
   if (a.splits > 1) {
     if (weight != 0.f)  // (else the join passes it by)
       *(f32x4*)(a.part + (((int64_t)z * a.tokens + r.token) * a.heads + r.head) * a.dim + d) = o;
     return;
   }
-  const float f = weight == 0.f ? 0.f : 1.f / weight;
-  o = weight == 0.f ? f32x4{} : o * f;
+  if (weight == 0.f) o = f32x4{};
   const int64_t at = (int64_t)r.token * a.ldy + r.head * a.dim + d;
   if (a.y_bf16)
     *(u32x2*)((uint16_t*)a.y + at) = u32x2{pack(o.x, o.y), pack(o.z, o.w)};
@@ -516,7 +520,8 @@ __device__ __forceinline__ void put_row(const AttendArgs& a, const Row& r, int z
 // A wave's rows (row0 .. row0 + 31 of sequence b and head kvh) done again, over blocks
 // w, w + step, ... of the parts of the keys that begin at `first` and lie `stride` apart,
 // each `chunk` long, up to block last.  A function of its own that is told as little as
-// possible: it is hardly ever called, and its registers are not the kernels'.
+// possible: it is hardly ever called, and its registers are not the kernels'.  Its sums
+// (not their weight) are times kLess.
 template <int D, int MODE>
 __device__ __attribute__((noinline)) void careful(const AttendArgs* args, int b, int kvh, int row0, int first, int chunk,
                                                   int stride, int last, int w, int step, Sums<D>* out) {
@@ -549,17 +554,18 @@ __device__ __attribute__((noinline)) void careful(const AttendArgs* args, int b,
   *out = c;
 }
 
-// A wave's sums to their places.
+// A wave's sums times a factor, normalised, to their places.
 template <int D>
-__device__ __forceinline__ void put_all(const AttendArgs& a, const Row& r, int z, int half, Sums<D>& c) {
+__device__ __forceinline__ void put_all(const AttendArgs& a, const Row& r, int z, int half, Sums<D>& c, float times) {
   c.l += other_half(c.l);
   if (!r.live) return;
+  const float f = c.l == 0.f ? 0.f : 1.f / c.l * times;
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      put(a, r, z, t * 32 + 8 * i + 4 * half, f32x4{c.o[t][4 * i], c.o[t][4 * i + 1], c.o[t][4 * i + 2], c.o[t][4 * i + 3]},
-          c.l);
+      put(a, r, z, t * 32 + 8 * i + 4 * half,
+          f32x4{c.o[t][4 * i], c.o[t][4 * i + 1], c.o[t][4 * i + 2], c.o[t][4 * i + 3]} * f, c.l);
   if (half == 0) put_row(a, r, z, c.m, c.l);
 }
 

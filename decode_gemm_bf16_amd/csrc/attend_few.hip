@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few
             const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][i], sc, -ref));
             const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][i + 1], sc, -ref));
             l[n] += p0 + p1;
-            p[i / 2] = pack(p0, p1);
+            p[i / 2] = again ? pack(p0 * kLess, p1 * kLess) : pack(p0, p1);
           }
           const bf16x8 weights = as_bf16x8(p[0], p[1], p[2], p[3]);
 #pragma unroll
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few
         }
       }
     }
-    // the waves' sums, brought to one maximum
+    // the waves' sums, brought to one maximum and normalised
 #pragma unroll
     for (int n = 0; n < R; ++n) {
       l[n] = sum_of_row(l[n]);
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(64 * few_waves(D), D > 128 ? 1 : 2) void attend_few
         const float e = share[1][i][col];
         weight += e == 0.f ? 0.f : e * __builtin_amdgcn_exp2f(share[0][i][col] - ref);
       }
-      const float f = __builtin_amdgcn_exp2f(m[n] - ref);
+      const float f = weight == 0.f ? 0.f : __builtin_amdgcn_exp2f(m[n] - ref) * (1.f / weight) * (again ? kMore : 1.f);
 #pragma unroll
       for (int t0 = 0; t0 < kTiles; t0 += kRound) {
         if (t0) __syncthreads();

@@ -357,13 +357,15 @@ __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kern
     }
     arrive();  // (of tiles behind the end, too: nothing is written to LDS later on)
   }
+  float times = 1.f;
   if (not_finite(c.o, 16)) {
     Sums<D> again;
     careful<D, MODE>(kernel_args(), b, kvh, rt * kManyRows + w * 32, b0 + z * a.chunk, a.chunk, a.splits * a.chunk, b1, 0, 1,
                      &again);
     c = again;
+    times = kMore;
   }
-  put_all(a, r, z, half, c);
+  put_all(a, r, z, half, c, times);
 }
 
 template <int D, int MODE, bool EDGES>

@@ -71,7 +71,7 @@ struct AttendArgs {
   const uint64_t* mask;
   void* y;
   float* lse;    // [tokens, heads] or null
-  float* part;   // [splits][tokens * heads][dim] sums, then [splits][tokens * heads][2] maximum and weight
+  float* part;   // [splits][tokens * heads][dim] rows, then [splits][tokens * heads][2] maximum and weight
   int64_t ldq, ldy, ldt;
   int32_t tokens, seqs, heads, kv_heads, group, dim, page_log2, pages, max_pages, words, window;
   int32_t rows;    // of one sequence and head of the cache that the call is laid out for

@@ -549,7 +549,10 @@ typedef struct {
  * and as key, at lengths[b] - n + (set bits of its row) - 1.  slopes_dev: float
  * [heads].  A token that sees no key gets y = 0 and lse -inf, as does one whose
  * scores are all -inf.  Infinities and NaN of keys and values reach the tokens that
- * see them and no others (an infinite value whose weight underflows gives NaN).
+ * see them and no others (an infinite value whose weight underflows gives NaN).  Finite values give
+ * finite results, as their mean is (within a bf16's half step of the largest bf16 it may
+ * round to an infinity); where sums on the way are not, weights below 2^-86 of a row's
+ * largest may count as 0.
  * q_dev bf16 [tokens, heads * dim], row stride ldq (a multiple of 8); y_dev of
  * y_type (UW_BF16, or UW_F32), row stride ldy (a multiple of 8); lse_dev float
  * [tokens, heads]: the logarithm of the sum of exp(x), or NULL.  Scores and sums are

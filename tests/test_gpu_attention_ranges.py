@@ -1,9 +1,10 @@
 """Attention at the ends of its arguments' ranges (GPU): marks that hide everything, caps far
-above and far below the scores; each laid out so that the kernel for few rows, the one for
-many with one part of the keys and with many take it."""
+above and far below the scores, values near the largest bf16; each laid out so that the
+kernel for few rows, the one for many with one part of the keys and with many take it."""
 import numpy as np
 import pytest
 
+import synth
 import test_gpu_attention as cases
 from test_gpu_attention import Cache, bf16, env  # noqa: F401
 
@@ -66,3 +67,29 @@ def test_caps(env, how, dim, cap, kw):  # noqa: F811
         a[7] = 0  # (scores of zero)
     cases.run(env, rng, counts, lengths, 4, 1, dim, 32, cache=one_long(rng, lengths, 1, dim, 32), q=q, cap=cap, out="f32",
               **kw, **sizes)
+
+
+@pytest.mark.parametrize("how", LAID_OUT)
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0), dict(window=200), dict(slopes=[0.01, 0.0, 0.0, 0.1])])
+def test_large_values(env, how, dim, kw):  # noqa: F811
+    """Values of 2^127, whose unnormalised sums pass float32's range: their mean does not."""
+    rng = np.random.default_rng(dim + 2)
+    for count, length in ((40, 300), (8 if how == "few" else 10, 2500)):
+        counts, lengths, sizes = laid_out(how, count, length, 4, 1)
+        c = one_long(rng, lengths, 1, dim, 32)
+        sign = rng.random(dim) < 0.5  # one sign an element: nothing cancels
+        for p in range(length):
+            row = np.where(sign, -1, 1) * np.float32(2.0 ** 127) * rng.uniform(0.9, 1.0, dim)
+            c.set_row(0, p, 0, False, synth.f32_to_bf16_bits(row.astype(np.float32)))
+        q = bf16(rng, count + 1, 4 * dim)
+        for out in ("bf16", "f32"):
+            y, _ = cases.run(env, rng, counts, lengths, 4, 1, dim, 32, cache=c, q=q, out=out, **kw, **sizes)
+            assert np.isfinite(y).all()
+    # a few of them, seen by some tokens only, beside ordinary ones
+    counts, lengths, sizes = laid_out(how, 40, 300, 4, 1)
+    c = one_long(rng, lengths, 1, dim, 32)
+    for p in (5, 250, 280, 299):
+        c.set_row(0, p, 0, False, synth.f32_to_bf16_bits(np.full(dim, 2.0 ** 127, dtype=np.float32)))
+    y, _ = cases.run(env, rng, counts, lengths, 4, 1, dim, 32, cache=c, **kw, **sizes)
+    assert np.isfinite(y).all()
