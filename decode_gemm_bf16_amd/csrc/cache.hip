@@ -117,12 +117,14 @@ struct Factors {
   }
 };
 
+// The first `turn` of 8 elements are turned (8 and more: all); the others stay, infinities, NaN
+// and signs of zero included.
 template <bool BF16>
-__device__ __forceinline__ u32x4 turned(Kind kind, const Piece<BF16>& p, const Factors& f) {
+__device__ __forceinline__ u32x4 turned(Kind kind, int turn, const Piece<BF16>& p, const Factors& f) {
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    y[e] = kind == kStay ? p.x[e] : p.x[e] * f.c[e] + (kind == kWithin ? p.x[e ^ 1] : p.z[e]) * f.s[e];
+    y[e] = kind == kStay || e >= turn ? p.x[e] : p.x[e] * f.c[e] + (kind == kWithin ? p.x[e ^ 1] : p.z[e]) * f.s[e];
   return u32x4{pack(y[0], y[1]), pack(y[2], y[3]), pack(y[4], y[5]), pack(y[6], y[7])};
 }
 
@@ -146,6 +148,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheWriteArgs a, int 
     const void* const from = keys ? a.k : a.q;
     const int64_t ld = keys ? a.ldk : a.ldq;
     const Kind kind = kind_of(a, c);
+    const int turn = 2 * a.pairs - 8 * c;
     f32x2* const table = (f32x2*)lds;
     auto place = [&](int i) { return keys ? a.slots[t0 + i] : 0; };
     auto put = [&](int i, int h, int slot, const u32x4& v) {
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheWriteArgs a, int 
       f.load(a, kind, table, c);
       for (int h = first; h < hs; h += kAtOnce) {
         if (h != first) p.load(a, kind, from, t0 * ld + (h0 + h) * kDim, c);
-        put(0, h0 + h, slot, turned(kind, p, f));
+        put(0, h0 + h, slot, turned(kind, turn, p, f));
       }
     } else {
       turns(a, t0, n, table);
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheWriteArgs a, int 
 #pragma unroll 2
         for (int h = 0; h < hs; ++h) {
           p.load(a, kind, from, (t0 + i) * ld + (h0 + h) * kDim, c);
-          put(i, h0 + h, slot, turned(kind, p, f));
+          put(i, h0 + h, slot, turned(kind, turn, p, f));
         }
       }
     }
