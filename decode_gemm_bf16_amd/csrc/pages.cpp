@@ -6,7 +6,6 @@
 #include <cstdio>
 #include <functional>
 #include <new>
-#include <queue>
 #include <vector>
 
 #include "../../include/uw.h"
@@ -14,10 +13,10 @@
 
 struct uw_page_counts {
   std::vector<int32_t> count;  // tables that hold a page; 0: free
-  // Pages from `fresh` on have not been taken yet; the free ones before it are in `freed`,
-  // lowest first.
+  // Pages from `fresh` on have not been taken yet; the free ones before it are in `freed`, a
+  // heap with the lowest in front and room for every page: freeing one cannot fail.
   int64_t fresh = 0;
-  std::priority_queue<int32_t, std::vector<int32_t>, std::greater<int32_t>> freed;
+  std::vector<int32_t> freed;
   int64_t used = 0;
 };
 
@@ -39,8 +38,9 @@ bool taken(const uw_page_counts* p, int32_t page) {
 int32_t take_one(uw_page_counts* p) {
   int32_t page;
   if (!p->freed.empty()) {
-    page = p->freed.top();
-    p->freed.pop();
+    page = p->freed.front();
+    std::pop_heap(p->freed.begin(), p->freed.end(), std::greater<int32_t>());
+    p->freed.pop_back();
   } else {
     page = (int32_t)p->fresh++;
   }
@@ -51,7 +51,8 @@ int32_t take_one(uw_page_counts* p) {
 
 void drop_one(uw_page_counts* p, int32_t page) {
   if (--p->count[page] > 0) return;
-  p->freed.push(page);
+  p->freed.push_back(page);
+  std::push_heap(p->freed.begin(), p->freed.end(), std::greater<int32_t>());
   --p->used;
 }
 
@@ -82,6 +83,7 @@ uw_status uw_pages_create(int64_t pages, uw_pages* out) {
     uw_page_counts* p = new uw_page_counts;
     try {
       p->count.assign(size_t(pages), 0);
+      p->freed.reserve(size_t(pages));
     } catch (...) {
       delete p;
       throw;
@@ -160,7 +162,7 @@ uw_status uw_pages_compact(uw_pages p, int32_t* src, int32_t* dst, int64_t* n) {
       dst[moves++] = (int32_t)to;
     }
     p->fresh = used;
-    p->freed = {};
+    p->freed.clear();
     *n = moves;
     return UW_OK;
   });
