@@ -60,8 +60,8 @@ uw_status check_apart(const Span* s, int outs, int all) {
   return UW_OK;
 }
 
-uw_status check_cache(const uw_cache_config* c, const void* k, const void* v) {
-  if (!c || !k || !v) return fail(UW_ERR_INVALID_ARG, "null argument");
+uw_status check_cache_sizes(const uw_cache_config* c) {
+  if (!c) return fail(UW_ERR_INVALID_ARG, "null argument");
   if (c->kv_heads < 1 || c->kv_heads > 128) return fail(UW_ERR_SHAPE, "kv_heads = %d must be 1..128", c->kv_heads);
   if (c->dim != 64 && c->dim != 96 && c->dim != 128 && c->dim != 256)
     return fail(UW_ERR_SHAPE, "dim = %d must be 64, 96, 128 or 256", c->dim);
@@ -69,6 +69,13 @@ uw_status check_cache(const uw_cache_config* c, const void* k, const void* v) {
     return fail(UW_ERR_SHAPE, "page = %d must be 32, 64, 128 or 256", c->page);
   if (c->pages < 1 || c->pages > kMaxPlaces / c->page)
     return fail(UW_ERR_INVALID_ARG, "pages = %lld out of range", (long long)c->pages);
+  return UW_OK;
+}
+
+uw_status check_cache(const uw_cache_config* c, const void* k, const void* v) {
+  if (!c || !k || !v) return fail(UW_ERR_INVALID_ARG, "null argument");
+  const uw_status st = check_cache_sizes(c);
+  if (st != UW_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(UW_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
   return UW_OK;
 }
@@ -113,8 +120,7 @@ uw_status check_sequences(int64_t seqs, int64_t ldt, int64_t max_pages) {
   return UW_OK;
 }
 
-uw_status check_attend_sizes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
-                             int64_t max_tokens, int64_t max_length) {
+uw_status check_attend_sizes(int64_t tokens, int64_t max_tokens, int64_t max_length) {
   if (max_tokens < 1 || max_tokens > tokens || max_length < 1 || max_length > (int64_t(1) << 30))
     return fail(UW_ERR_INVALID_ARG, "max_tokens must be 1..tokens and max_length 1..2^30");
   return UW_OK;
@@ -123,6 +129,15 @@ uw_status check_attend_sizes(int64_t tokens, int64_t seqs, int32_t heads, int32_
 }  // namespace
 
 namespace uw {
+
+uw_status attention_sizes_check(const uw_cache_config* config, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                                int64_t max_length) {
+  uw_status st = check_cache_sizes(config);
+  if (st != UW_OK || (st = check_heads(config)) != UW_OK || (st = check_tokens(tokens)) != UW_OK ||
+      (st = check_sequences(seqs, 1, 1)) != UW_OK)
+    return st;
+  return check_attend_sizes(tokens, max_tokens, max_length);
+}
 
 uw_status cache_write_prepare(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev, int64_t ldq,
                               const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
@@ -203,7 +218,7 @@ uw_status attend_prepare(const uw_cache_config* config, const uw_attend_config* 
     return fail(UW_ERR_INVALID_ARG, "null argument");
   if ((st = check_heads(config)) != UW_OK || (st = check_tokens(tokens)) != UW_OK ||
       (st = check_sequences(seqs, ldt, max_pages)) != UW_OK ||
-      (st = check_attend_sizes(tokens, seqs, c.heads, c.kv_heads, c.dim, max_tokens, max_length)) != UW_OK)
+      (st = check_attend_sizes(tokens, max_tokens, max_length)) != UW_OK)
     return st;
   if (y_type != UW_F32 && y_type != UW_BF16) return fail(UW_ERR_INVALID_ARG, "unknown output type %d", y_type);
   if (!std::isfinite(options->scale) || options->scale <= 0.f)
@@ -296,10 +311,7 @@ uw_status uw_cache_write(const uw_cache_config* config, const uw_rotary* rotary,
 size_t uw_attend_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
                                  int64_t max_tokens, int64_t max_length) {
   const uw_cache_config c = {heads, kv_heads, dim, 32, 1};
-  if (check_cache(&c, &c, &c) == UW_ERR_SHAPE || check_heads(&c) != UW_OK || check_tokens(tokens) != UW_OK ||
-      check_sequences(seqs, 1, 1) != UW_OK ||
-      check_attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length) != UW_OK)
-    return 0;
+  if (uw::attention_sizes_check(&c, tokens, seqs, max_tokens, max_length) != UW_OK) return 0;
   return uw::attend_plan(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length).bytes;
 }
 

@@ -1390,8 +1390,10 @@ uw_status attention_impl(uw_handle q, uw_handle k, uw_handle v, uw_handle o, con
   const uw_handle hs[4] = {q, k, v, o};
   for (int j = 1; j < 4; ++j)
     if (hs[j]->main != q->main) return fail(UW_ERR_INVALID_ARG, "q, k, v and o must share one main stream");
-  const size_t need = uw_attention_workspace_bytes(config, b.tokens, b.seqs, b.max_tokens, b.max_length);
-  if (need == 0) return fail(UW_ERR_INVALID_ARG, "tokens, seqs, max_tokens, max_length or heads out of range");
+  uw_status st = uw::attention_sizes_check(config, b.tokens, b.seqs, b.max_tokens, b.max_length);
+  if (st != UW_OK) return st;
+  const AttentionParts p = attention_parts(*config, b.tokens, b.seqs, b.max_tokens, b.max_length);
+  const size_t need = p.total;
   const uintptr_t wa = reinterpret_cast<uintptr_t>(work), xa = reinterpret_cast<uintptr_t>(x),
                   ya = reinterpret_cast<uintptr_t>(y), ka = reinterpret_cast<uintptr_t>(kc),
                   va = reinterpret_cast<uintptr_t>(vc);
@@ -1401,10 +1403,8 @@ uw_status attention_impl(uw_handle q, uw_handle k, uw_handle v, uw_handle o, con
     return fail(UW_ERR_INVALID_ARG, "workspace of %zu bytes, the layer needs %zu", work_bytes, need);
   int ps[4];
   uw::Variant vs[4];
-  uw_status st;
   for (int j = 0; j < 4; ++j)
     if ((st = matmul_check(hs[j], x, y, b.tokens, pipelines[j], &ps[j], &vs[j])) != UW_OK) return st;
-  const AttentionParts p = attention_parts(*config, b.tokens, b.seqs, b.max_tokens, b.max_length);
   uint8_t* const m = static_cast<uint8_t*>(work);
   float *qf = reinterpret_cast<float*>(m + p.q), *kf = reinterpret_cast<float*>(m + p.k),
         *vf = reinterpret_cast<float*>(m + p.v);
@@ -1608,11 +1608,7 @@ uw_status uw_moe_forward(const uw_handle* handles, const int32_t* pipelines, con
 
 size_t uw_attention_workspace_bytes(const uw_cache_config* config, int64_t tokens, int64_t seqs, int64_t max_tokens,
                                     int64_t max_length) {
-  if (!config || tokens < 1 || tokens > (int64_t(1) << 20) || config->heads < 1 || config->heads > 256 ||
-      config->kv_heads < 1 || config->kv_heads > 128 || config->dim < 1 || config->dim > 256 || max_tokens < 1 ||
-      max_tokens > tokens || max_length < 1 || max_length > (int64_t(1) << 30) || seqs < 1 || seqs > 65535 ||
-      config->heads % config->kv_heads)
-    return 0;
+  if (uw::attention_sizes_check(config, tokens, seqs, max_tokens, max_length) != UW_OK) return 0;
   return attention_parts(*config, tokens, seqs, max_tokens, max_length).total;
 }
 

@@ -23,6 +23,9 @@ uw_status route_check(const void* logits, int32_t type, int64_t ld, int64_t toke
 uw_status route_launch(const void* logits, int32_t type, int64_t ld, int64_t tokens, const float* bias,
                        const uw_route_config* c, int32_t* experts, float* weights, hipStream_t s);
 
+// The sizes that uw_attend_workspace_bytes and uw_attention_workspace_bytes take (attention.cpp).
+uw_status attention_sizes_check(const uw_cache_config* config, int64_t tokens, int64_t seqs, int64_t max_tokens,
+                                int64_t max_length);
 // uw_cache_write's and uw_attend's checks, and their kernels' arguments (attention.cpp).
 uw_status cache_write_prepare(const uw_cache_config* config, const uw_rotary* rotary, const void* q_dev,
                           int64_t ldq, const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv, int32_t type,
