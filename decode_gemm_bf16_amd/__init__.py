@@ -694,7 +694,12 @@ def _cache_config(heads, kv_heads, dim, page, pages) -> CacheConfig:
 
 @functools.lru_cache(maxsize=64)
 def _attend_config(scale, cap, window) -> AttendConfig:
-    return AttendConfig(scale, cap, window)
+    c = AttendConfig(scale, cap, window)  # (its types cut what they cannot hold)
+    if c.window != window:
+        raise ValueError(f"window must be 0..2^31-1, not {window}")
+    if cap and not c.cap:
+        raise ValueError(f"cap must be 0 or a float32 above it, not {cap}")
+    return c
 
 
 @functools.lru_cache(maxsize=64)

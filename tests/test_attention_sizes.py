@@ -1,7 +1,8 @@
-"""Workspace sizes of arguments out of range (CPU)."""
+"""Workspace sizes of arguments out of range, and numbers that the C types cannot hold (CPU)."""
 import ctypes as C
 
 import pytest
+import torch
 
 import decode_gemm_bf16_amd as uw
 
@@ -22,3 +23,23 @@ def test_layer_workspace_out_of_range(kw):
     if not {"page", "pages"} & kw.keys():
         for f in (uw.attention_workspace_bytes, uw.attend_workspace_bytes):
             assert f(d["tokens"], d["seqs"], d["heads"], d["kv_heads"], d["dim"], d["max_tokens"], d["max_length"]) == 0
+
+
+FAR = 1 << 32  # (cut to 32 bits: 0)
+
+
+@pytest.mark.parametrize("window", [FAR, FAR + 5, 2 ** 31, -2 ** 31 - 1, FAR - 1])
+def test_a_window_is_not_cut(window):
+    kc = torch.zeros((3, 2, 32, 64), dtype=torch.bfloat16)
+    q, i, table = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32)
+    with pytest.raises(ValueError, match="window"):
+        uw.attend(q, kc, kc, i, i[:3], table, q, window=window)
+
+
+@pytest.mark.parametrize("cap", [1e-50, 5e-46])
+def test_a_cap_is_not_cut(cap):
+    """(a cap of 0 would be none)"""
+    kc = torch.zeros((3, 2, 32, 64), dtype=torch.bfloat16)
+    q, i, table = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32)
+    with pytest.raises(ValueError, match="cap"):
+        uw.attend(q, kc, kc, i, i[:3], table, q, cap=cap)
