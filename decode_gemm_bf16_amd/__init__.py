@@ -769,14 +769,14 @@ def attend(q, kc, vc, offsets, lengths, tables, y, work=None, scale: float | Non
     shape = pages, kv, page, dim = _cache_shape(kc, 4)
     rows = t, cols = _shape2(q, "q")
     heads = _heads(cols, dim, "q")
+    config = _attend_config(dim ** -0.5 if scale is None else scale, cap, window)
     qp, ldq = _rows(q, "q", _bf16, rows, dev)
     yp, ldy = _rows(y, "y", _either, rows, dev)
     table = n, reach = _shape2(tables, "tables")
     tp, ldt = _rows(tables, "tables", _i32, table, dev)
     words = 0 if mask is None else _shape2(mask, "mask")[1]
     wp, wb = _bytes(work, "work", dev)
-    _check(_lib.uw_attend(_cache_config(heads, kv, dim, page, pages),
-                          _attend_config(dim ** -0.5 if scale is None else scale, cap, window), qp, ldq,
+    _check(_lib.uw_attend(_cache_config(heads, kv, dim, page, pages), config, qp, ldq,
                           _tensor(kc, "kc", _bf16, shape, dev), _tensor(vc, "vc", _bf16, shape, dev),
                           _tensor(offsets, "offsets", _i32, (n + 1,), dev),
                           _tensor(lengths, "lengths", _i32, (n,), dev), tp, ldt, reach,
@@ -891,6 +891,7 @@ def attention_forward(q: Matrix, k: Matrix, v: Matrix, o: Matrix, pipelines, x, 
     if hidden != q.cols:
         raise ValueError(f"x must have {q.cols} columns, not {hidden}")
     heads = _heads(q.rows, dim, "q's output")
+    config = _attend_config(dim ** -0.5 if scale is None else scale, cap, window)
     axes = _shape2(positions, "positions")[0]
     pairs = freqs.numel()
     table = n, reach = _shape2(tables, "tables")
@@ -907,7 +908,6 @@ def attention_forward(q: Matrix, k: Matrix, v: Matrix, o: Matrix, pipelines, x, 
         t if max_tokens is None else max_tokens, reach * page if max_length is None else max_length, ldt, reach, words)
     wp, wb = _bytes(work, "work", dev)
     _check(_lib.uw_attention_forward(q._h, k._h, v._h, o._h, (C.c_int32 * 4)(*pipelines),
-                                     _cache_config(heads, kv, dim, page, pages), _rotary(axes, pairs, adjacent),
-                                     _attend_config(dim ** -0.5 if scale is None else scale, cap, window), batch,
+                                     _cache_config(heads, kv, dim, page, pages), _rotary(axes, pairs, adjacent), config, batch,
                                      _tensor(x, "x", _bf16, rows, dev), _tensor(kc, "kc", _bf16, shape, dev),
                                      _tensor(vc, "vc", _bf16, shape, dev), _tensor(y, "y", _f32, rows, dev), wp, wb))
