@@ -686,6 +686,24 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
 # layers' [layers, pages, kv_heads, page, dim] (kc[l] is one layer's).  Within a page
 # of a head the elements are in the order of the matrix operands (include/uw.h).
 
+_INT32, _INT64 = range(-2 ** 31, 2 ** 31), range(-2 ** 63, 2 ** 63)
+
+
+def _attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length) -> bool:
+    """Whether the C types hold them: they cut others, and 0 bytes are the answer to those."""
+    return all(v in _INT64 for v in (tokens, seqs, max_tokens, max_length)) and all(v in _INT32 for v in (heads, kv_heads, dim))
+
+
+def _page_list(pages) -> np.ndarray:
+    a = np.asarray(pages)
+    if a.size == 0:
+        return np.empty(0, dtype=np.int32)
+    if a.dtype.kind not in "iu":
+        raise TypeError(f"pages must be whole numbers, not {a.dtype}")
+    if int(a.min()) not in _INT32 or int(a.max()) not in _INT32:
+        raise ValueError("a page's number must be that of one of the cache's pages")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
 
 @functools.lru_cache(maxsize=256)
 def _cache_config(heads, kv_heads, dim, page, pages) -> CacheConfig:
@@ -753,7 +771,8 @@ def cache_write(q, k, v, positions, freqs, slots, qr, kc, vc, axis=None, adjacen
 
 def attend_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int, max_tokens: int,
                            max_length: int) -> int:
-    return _lib.uw_attend_workspace_bytes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length)
+    sizes = tokens, seqs, heads, kv_heads, dim, max_tokens, max_length
+    return _lib.uw_attend_workspace_bytes(*sizes) if _attend_sizes(*sizes) else 0
 
 
 def attend(q, kc, vc, offsets, lengths, tables, y, work=None, scale: float | None = None, cap: float = 0.0,
@@ -823,6 +842,8 @@ class Pages:
     def __init__(self, pages: int):
         h = C.c_void_p()
         self._h = h
+        if pages not in _INT64:
+            raise ValueError(f"pages must be 1..2^26, not {pages}")
         _check(_lib.uw_pages_create(pages, C.byref(h)))
         self.pages = pages
 
@@ -831,26 +852,30 @@ class Pages:
         return _lib.uw_pages_left(self._h)
 
     def holders(self, page: int) -> int:
-        return _lib.uw_pages_holders(self._h, page)
+        return _lib.uw_pages_holders(self._h, page) if page in _INT32 else 0
 
     def take(self, n: int) -> np.ndarray:
         """The n lowest free pages."""
-        out = np.empty(max(n, 0), dtype=np.int32)
+        if n not in _INT64:
+            raise ValueError(f"n must be 0..{self.pages}, not {n}")
+        out = np.empty(min(max(n, 0), self.pages), dtype=np.int32)
         _check(_lib.uw_pages_take(self._h, n, out.ctypes.data))
         return out
 
     def share(self, pages) -> None:
         """A fork: each page is held once more."""
-        a = np.ascontiguousarray(pages, dtype=np.int32)
+        a = _page_list(pages)
         _check(_lib.uw_pages_share(self._h, a.ctypes.data, a.size))
 
     def drop(self, pages) -> None:
         """Each page is held once less; free where nobody holds it."""
-        a = np.ascontiguousarray(pages, dtype=np.int32)
+        a = _page_list(pages)
         _check(_lib.uw_pages_drop(self._h, a.ctypes.data, a.size))
 
     def own(self, page: int) -> int:
         """The page to write in place of ``page``: itself, or a new one to copy it to."""
+        if page not in _INT32:
+            raise ValueError(f"page must be one of the {self.pages}, not {page}")
         out = C.c_int32()
         _check(_lib.uw_pages_own(self._h, page, C.byref(out)))
         return out.value
@@ -875,6 +900,8 @@ class Pages:
 
 def attention_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int, max_tokens: int,
                               max_length: int) -> int:
+    if not _attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length):
+        return 0
     return _lib.uw_attention_workspace_bytes(CacheConfig(heads, kv_heads, dim, 32, 1), tokens, seqs, max_tokens, max_length)
 
 

@@ -1,6 +1,7 @@
 """Workspace sizes of arguments out of range, and numbers that the C types cannot hold (CPU)."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
@@ -43,3 +44,28 @@ def test_a_cap_is_not_cut(cap):
     q, i, table = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32)
     with pytest.raises(ValueError, match="cap"):
         uw.attend(q, kc, kc, i, i[:3], table, q, cap=cap)
+
+
+@pytest.mark.parametrize("kw", [dict(heads=FAR + 8), dict(kv_heads=FAR + 2), dict(dim=FAR + 64), dict(tokens=(1 << 64) + 6)])
+def test_sizes_are_not_cut(kw):
+    d = dict(tokens=6, seqs=2, heads=8, kv_heads=2, dim=64, max_tokens=3, max_length=5000)
+    d.update(kw)
+    for f in (uw.attention_workspace_bytes, uw.attend_workspace_bytes):
+        assert f(**d) == 0
+
+
+def test_pages_are_not_cut():
+    p = uw.Pages(4)
+    p.take(2)
+    far = np.array([FAR + 1])
+    for f, bad in ((p.share, far), (p.share, [FAR]), (p.drop, far), (p.drop, [FAR]), (p.share, [0.5]), (p.drop, np.array([1.0])),
+                   (p.share, np.array([True])), (p.own, FAR), (p.own, 1 - FAR), (p.take, (1 << 64) + 1)):
+        with pytest.raises((ValueError, TypeError)):
+            f(bad)
+    assert p.holders(FAR) == p.holders(FAR + 1) == p.holders(-FAR) == 0
+    assert p.left == 2 and p.holders(0) == p.holders(1) == 1
+    p.share([])
+    p.drop(np.array([0, 1], dtype=np.uint8))
+    assert p.left == 4
+    with pytest.raises(ValueError):
+        uw.Pages((1 << 64) + 4)
