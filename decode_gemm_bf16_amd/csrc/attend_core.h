@@ -232,7 +232,7 @@ struct Cap {
 // The same for caps further off (kFar): up to u = scale x / cap = 1/2, as hardly any score
 // passes, it is scale x times a polynomial in u^2, fitted to tanh(u) / u - 1 within 0.3 * 2^-24,
 // so that its error is relative to the score; from there on the other form's is, too, 8 * 2^-23
-// of it at most.  A prompt of 8192 tokens 703 us, with the other form 668; where scores do pass
+// of it at most.  A prompt of 8192 tokens 712 us, with the other form 667; where scores do pass
 // 1/2 it costs more (trees of 61 tokens over 6000 keys at a cap of 8 234 against 171, prompts of
 // 4096 tokens with heads of 256 at 50 416 against 393), so near caps keep theirs.
 struct FarCap {
@@ -241,15 +241,16 @@ struct FarCap {
       : in(a.cap_in * (0.5f * kLn2)), scale(a.scale * kLog2e) {}
   // What is capped already stays as it is.
   __device__ __forceinline__ void pass() { in = 0.f, scale = 1.f; }
-  __device__ __forceinline__ float operator()(float x, float more) const {  // up to 1/2; and `more`
+  __device__ __forceinline__ float operator()(float x) const {  // up to 1/2
+#pragma clang fp contract(off)  // (one rounding wherever it is used: rows done again come out the same)
     const float u = x * in, z = u * u;
     float p = __builtin_fmaf(z, 0.01725699f, -0.05305295f);
     p = __builtin_fmaf(z, p, 0.13325988f);
     p = __builtin_fmaf(z, p, -0.3333315f);
-    return __builtin_fmaf(x * scale, __builtin_fmaf(z, p, 1.f), more);
+    return x * scale * __builtin_fmaf(z, p, 1.f);
   }
   __device__ __forceinline__ float any(const Cap& cap, float x) const {
-    return __builtin_fabsf(x * in) <= 0.5f ? (*this)(x, 0.f) : cap(x);
+    return __builtin_fabsf(x * in) <= 0.5f ? (*this)(x) : cap(x);
   }
   // Whether some product of a block passes 1/2.
   template <int N, typename X>

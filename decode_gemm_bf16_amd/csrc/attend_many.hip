@@ -136,16 +136,16 @@ struct Unit {
 #pragma unroll
           for (int e = 16 * i / kLead; e < 16 * (i + 1) / kLead; ++e) {
             if (MODE == (kCap | kSlopes)) x[e] = cap(x[e]);
-            if (MODE & kSlopes) {
-              const float slope = __builtin_fmaf(r.slope, (float)key_of(e), base);
-              x[e] = MODE & kFar ? far(x[e], slope) : __builtin_fmaf(x[e], MODE & kCap ? 1.f : a.scale * kLog2e, slope);
-            }
+            if (MODE == (kCap | kSlopes | kFar)) x[e] = far(x[e]);
+            if (MODE & kSlopes)
+              x[e] = __builtin_fmaf(x[e], MODE & kCap ? 1.f : a.scale * kLog2e,
+                                    __builtin_fmaf(r.slope, (float)key_of(e), base));
             top = __builtin_fmaxf(top, x[e]);
           }
           if (i == kLead - 1) {
             top = larger_half(top);
             if (MODE == kCap) top = cap(top);
-            if (MODE == (kCap | kFar)) top = far(top, 0.f);
+            if (MODE == (kCap | kFar)) top = far(top);
             if (MODE == 0) top *= sc;
             moved = __ballot(top > c.m + kSlack) != 0;
             const float was = c.m;
@@ -153,14 +153,14 @@ struct Unit {
             m = c.m == kNone ? 0.f : c.m;
             f = moved ? __builtin_amdgcn_exp2f(was - m) : 1.f;
             c.l *= f;
+            asm volatile("" : "+v"(c.l));  // (no fused sum: rows done again by careful() come out the same)
           }
         } else {
           constexpr int kRest = kAll - kLead;
 #pragma unroll
           for (int e = 16 * (i - kLead) / kRest; e < 16 * (i - kLead + 1) / kRest; ++e) {
-            const float y = MODE == 0                ? __builtin_fmaf(x[e], sc, -m)
-                            : MODE == (kCap | kFar) ? far(x[e], -m)
-                                                    : (MODE == kCap ? cap(x[e]) : x[e]) - m;
+            const float y = MODE == 0 ? __builtin_fmaf(x[e], sc, -m)
+                                      : (MODE == kCap ? cap(x[e]) : MODE == (kCap | kFar) ? far(x[e]) : x[e]) - m;
             const float now = __builtin_amdgcn_exp2f(y);
             if (e % 2) {
               c.l += last + now;
