@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import synth
+import test_gpu_attention as cases
 from oracle import attention as att
 from test_gpu_attention import INF, NAN, env, i32  # noqa: F401
 
@@ -40,3 +41,12 @@ def test_what_is_not_turned_stays(env, tokens, type, pairs, adjacent):  # noqa: 
 
     check(uw.bits_of(qr).reshape(tokens, heads, dim), heads)
     check(att.read_cache(uw.bits_of(kc), np.arange(pages), tokens, True, absent=0), kv)
+
+
+@pytest.mark.parametrize("tokens", [512, 777, 1023, 6001])
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv,dim,page,axes,pairs,adjacent", [(4, 2, 64, 32, 1, 32, False), (6, 6, 96, 32, 2, 17, False),
+                                                                   (4, 1, 256, 128, 4, 128, True)])
+def test_tiles_of_all_sizes(env, tokens, type, heads, kv, dim, page, axes, pairs, adjacent):  # noqa: F811
+    """Tiles of 8 tokens and of 32 with many heads each, over slots in runs and in no order."""
+    cases.test_write(env, tokens, type, heads, kv, dim, page, axes, pairs, adjacent)
