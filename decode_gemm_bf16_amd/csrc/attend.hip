@@ -7,7 +7,7 @@ namespace {
 // ---- the parts of split keys, joined ----
 //
 // A workgroup joins 8 rows, 32 lanes each, or one row whose parts its 8 groups of 32
-// lanes divide (ONE).  Up to 32 parts, and 256: a lane has each part's maximum and weight;
+// lanes divide (ONE).  Up to 8 parts, and 256: a lane has each part's maximum and weight;
 // then 4 elements of 32 columns a lane (H: twice, of long heads), the loads of
 // several parts in flight.
 __device__ __forceinline__ float max32(float v) {
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
           if (ONE)
             g[k] = z < a.splits ? factor[z] : -1.f;
           else
-            g[k] = __shfl(f, (threadIdx.x & 32) + (z < 32 ? z : 31), 64);
+            g[k] = __shfl(f, (threadIdx.x & 32) + z, 64);
           if (z >= a.splits) g[k] = -1.f;
 #pragma unroll
           for (int i = 0; i < H; ++i) {
@@ -132,11 +132,19 @@ void join(const AttendArgs& a, dim3 grid, hipStream_t s) {
 // of them where the whole call is up to 256 workgroups of 32 rows and the keys are short:
 // eight waves divide a workgroup's keys there, which takes less time from the first key to
 // the last than 128 rows that walk them all (one sequence of 24 tokens, 32 heads of 128 on 8:
-// 200 keys 19.5 -> 14.4 us, 600 19.4 -> 13.4; 61 tokens, 6000 keys 32.5 -> 29.1; but 30000
-// keys 44 -> 73, and 24 keys 9.5 -> 11).  Heads of 256 turn earlier (2000 keys 61 -> 66).
+// 200 keys 16.6 -> 12.4 us, 600 19.2 -> 13.1; 61 tokens, 6000 keys 29.7 -> 28.4; four of 61
+// over 2000 29.9 -> 27.1; but 30000 keys 39 -> 73, and 24 keys 10.8 -> 11.3).  The bounds are not
+// the best everywhere: 240 tokens over 5000 keys, 240 workgroups, lose (43 -> 56), and heads of
+// 256 would gain past theirs (24 tokens over 2000 keys 43 -> 33).
 //
 // Parts of the keys: enough workgroups to fill the chip, two a unit of the kernel for many
-// rows and one of the other, of at least so many keys that joining them is worth it.
+// rows and one of the other, of at least so many keys that joining them is worth it.  Few rows
+// over up to 48 blocks stay in one part: the join's launch costs more than it gives one sequence
+// (700 keys 11.0 us, in parts 14.0; 1500 keys 12.2 and 13.7; but eight of 1500 19.7 and 16.7).
+// Parts go by the call's sizes alone: where 256 workgroups are reached without them, one long
+// context among short ones is walked by one workgroup a key head (63 sequences of 500 keys and
+// one of 131072: 1110 us), and a last round of few workgroups costs a whole one (32 sequences of
+// 8192 keys 161 us, 40 of them 238, 64 315).
 AttendPlan plan_for(int64_t tokens, int64_t seqs, int64_t group, int64_t kv_heads, int64_t dim, int64_t max_tokens,
                     int64_t blocks) {
   AttendPlan p;

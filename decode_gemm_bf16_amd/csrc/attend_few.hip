@@ -26,9 +26,9 @@ __device__ __forceinline__ float sum_of_row(float v) {
 // registers of the products (lines of 128 bytes whole).  A wave takes every eighth block
 // of 32 keys; the keys of the next block are on their way during the softmax, its
 // values during the next product.  64 sequences of up to 8192 keys, 32 heads of 128 on 8:
-// 192 us (5.8 TB/s; with four waves 216, with cached loads 262 against 234); two of 131072
-// 161 us (6.5 TB/s; four waves 184).  Heads of 256 fill 512 registers and have four waves
-// (32 sequences of 8192 keys 315 us, 6.8 TB/s, against 366 with eight; two tiles of rows 190
+// 194 us (5.7 TB/s; with four waves 216, with cached loads 262 against 234); two of up to 131072
+// 162 us (6.4 TB/s; four waves 184).  Heads of 256 fill 512 registers and have four waves
+// (32 sequences of 8192 keys 315 us, 6.8 TB/s, against 366 with eight; two tiles of rows 194
 // against 479).
 //
 // A workgroup has up to 32 rows of a sequence and key head (R = 2; up to 16 one tile of

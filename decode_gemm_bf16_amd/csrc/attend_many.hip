@@ -201,14 +201,16 @@ struct Unit {
 // of block u, and the products with the values of block u - 1.  The three depend on
 // nothing of each other's, and the vector instructions of one hide, with two waves a SIMD,
 // behind half of the matrix instructions of the others (8 products of 32x32x16 131 ns, 96
-// FMA 110, both 187).  That bounds it: a prompt of 8192 tokens, 32 heads of 128 on 8, 521 us
-// (1.05 PFLOP/s; the library's matrix product reaches 1.2); with a cap, whose tanh is five
-// more instructions a score, trees of 61 tokens over 6144 keys 0.57 PFLOP/s.  64 rows a
+// FMA 110, both 187).  That bounds it: a prompt of 8192 tokens, 32 heads of 128 on 8, 514 to 544
+// us from card to card (1.01 to 1.07 PFLOP/s; the library's matrix product reaches 1.2), the
+// matrix units at work for 57 % of the cycles, waves waiting for loads, LDS and barriers 22 %
+// of theirs; with a cap, whose tanh is five more instructions a score, trees of 61 tokens over
+// 6000 keys 0.59 PFLOP/s, without one 0.75.  64 rows a
 // wave, which read LDS half as often, leave one wave a SIMD, and that issues vector
 // instructions at half the rate (722 us against 613, under a profiler).
 //
 // Heads of 256 have one wave a SIMD all the same: their sums take half of its registers
-// (prompt of 4096 tokens 410 us, 0.67 PFLOP/s).
+// (prompt of 4096 tokens 328 us, 0.84 PFLOP/s).
 template <int D, int MODE, bool EDGES>
 __global__ __launch_bounds__(64 * kWaves, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
   constexpr int kBytes = 64 * D;               // of a block's keys, or values
@@ -377,9 +379,10 @@ void launch_edges(const AttendArgs& a, hipStream_t s) {
 
 // EDGES where many blocks are seen in part: with documents, and with short heads, whose
 // 128 rows are 128 tokens of one head as a rule (24 chunks of up to 700 tokens, heads of 64,
-// a window: 104 -> 94 us; documents of 300 tokens, heads of 128: 85 -> 74).  Elsewhere its
-// branch costs more than it saves (chunks of 4 heads of 128 a key head: 221 -> 232), and the
-// places of a cap's scores are hidden after it.
+// a window: 95 -> 87 us, with slopes 116 -> 111; documents of 300 tokens 87 -> 77, heads of 64
+// 59 -> 51; a prompt with heads of 64 pays 328 -> 338).  Elsewhere its branch gives little or
+// takes some (chunks of 4 heads of 128 a key head 261 -> 260, with a window 204 -> 200; a prompt of
+// 8192 tokens 514 -> 523), and the places of a cap's scores are hidden after it.
 template <int D, int MODE>
 void launch(const AttendArgs& a, hipStream_t s) {
   if constexpr (MODE & kCap)

@@ -47,8 +47,10 @@ __device__ __forceinline__ float load1(const void* p, int64_t at) {
 // the angle, position times frequency, is formed and brought into one turn in 64 bits
 // (32 would lose 0.06 of a turn's radians at a position of 10^6), the functions are
 // float32.  A lane has 8 elements of a token's heads (and, where pairs lie apart, their
-// partners).  Bound by HBM: each row is read and written once (8191 tokens, 32 and 8
-// heads of 128 in bf16, 201 MB: 49.5 us, 4.1 TB/s); one token by the launch (2.8 us).
+// partners).  Each row is read and written once (8191 tokens, 32 and 8 heads of 128 in bf16,
+// 201 MB: 48.5 us, 4.2 TB/s, where a copy reaches 5.6): waves wait for memory 83 % of their time,
+// with nothing in flight from a head of the values to the next, and the one round of
+// workgroups leaves the CUs idle for a fifth of it.  One token by the launch (3.0 us).
 
 // cos and sin of the tile's tokens and pairs: table[i * pairs + j].
 __device__ __forceinline__ void turns(const CacheWriteArgs& a, int64_t t0, int n, f32x2* table) {
@@ -311,11 +313,13 @@ __global__ __launch_bounds__(256) void cache_copy_kernel(uint8_t* kc, uint8_t* v
 // One workgroup: one sequence and some heads of all layers.  A lane moves one
 // element of the values, or 8 of the keys, of every row of the list in order: entries
 // rise, so that row i's place is read by no later row, and 8 rows are in flight.  Bound by
-// the lines that single rows lie in (16 bytes of each 128 of the keys, 2 of each 16 of
-// the values) and the chain of list, table and rows; where a row stands is worked out
-// once, a lane adds its head and element.  64 sequences, up to 7 rows each, 32 layers of
-// 8 heads of 128: 84 us, 110 MB fetched and 78 written for 68 (1, 2, 4 and 8 heads a
-// workgroup in an earlier form: 95, 100, 108 and 120 us); one sequence 4 us.
+// latency: a workgroup is one chain of list, table, places and rows, and its waves wait for
+// memory 87 % of their time; each works out its sequence's places again (256 times a
+// sequence here), and 144 of its 256 lanes have rows to move.  64 sequences, up to 7 rows each,
+// 32 layers of 8 heads of 128: 84 us.  The traffic is less: 144 to 188 MB for the 68 of the rows
+// (which are 16 bytes of each 128 of the keys, 2 of each 16 of the values), 26 to 33 us at a
+// copy's rate.  1, 2, 4 and 8 heads a workgroup in an earlier form: 95, 100, 108 and 120 us; one
+// sequence 4 us.
 template <int C>
 __global__ __launch_bounds__(256) void cache_keep_kernel(CacheKeepArgs a, int per) {
   constexpr int kDim = 8 * C, kEach = kDim + C;  // a head's lanes: its values' elements, then its keys' chunks
