@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 import os
 
 import numpy as np
@@ -686,12 +687,15 @@ def lora_apply(adapters, plan, x, ys, work, bases=None, stream=None) -> None:
 # layers' [layers, pages, kv_heads, page, dim] (kc[l] is one layer's).  Within a page
 # of a head the elements are in the order of the matrix operands (include/uw.h).
 
-_INT32, _INT64 = range(-2 ** 31, 2 ** 31), range(-2 ** 63, 2 ** 63)
+
+def _fits(v, bits: int = 32) -> bool:
+    """Whether a whole number is one of so many bits (the C types cut others)."""
+    return -(1 << (bits - 1)) <= operator.index(v) < 1 << (bits - 1)
 
 
 def _attend_sizes(tokens, seqs, heads, kv_heads, dim, max_tokens, max_length) -> bool:
-    """Whether the C types hold them: they cut others, and 0 bytes are the answer to those."""
-    return all(v in _INT64 for v in (tokens, seqs, max_tokens, max_length)) and all(v in _INT32 for v in (heads, kv_heads, dim))
+    """Whether the C types hold them (0 bytes are the answer to others)."""
+    return all(_fits(v, 64) for v in (tokens, seqs, max_tokens, max_length)) and all(_fits(v) for v in (heads, kv_heads, dim))
 
 
 def _page_list(pages) -> np.ndarray:
@@ -700,7 +704,7 @@ def _page_list(pages) -> np.ndarray:
         return np.empty(0, dtype=np.int32)
     if a.dtype.kind not in "iu":
         raise TypeError(f"pages must be whole numbers, not {a.dtype}")
-    if int(a.min()) not in _INT32 or int(a.max()) not in _INT32:
+    if not _fits(a.min()) or not _fits(a.max()):
         raise ValueError("a page's number must be that of one of the cache's pages")
     return np.ascontiguousarray(a, dtype=np.int32)
 
@@ -842,7 +846,7 @@ class Pages:
     def __init__(self, pages: int):
         h = C.c_void_p()
         self._h = h
-        if pages not in _INT64:
+        if not _fits(pages, 64):
             raise ValueError(f"pages must be 1..2^26, not {pages}")
         _check(_lib.uw_pages_create(pages, C.byref(h)))
         self.pages = pages
@@ -852,11 +856,11 @@ class Pages:
         return _lib.uw_pages_left(self._h)
 
     def holders(self, page: int) -> int:
-        return _lib.uw_pages_holders(self._h, page) if page in _INT32 else 0
+        return _lib.uw_pages_holders(self._h, page) if _fits(page) else 0
 
     def take(self, n: int) -> np.ndarray:
         """The n lowest free pages."""
-        if n not in _INT64:
+        if not _fits(n, 64):
             raise ValueError(f"n must be 0..{self.pages}, not {n}")
         out = np.empty(min(max(n, 0), self.pages), dtype=np.int32)
         _check(_lib.uw_pages_take(self._h, n, out.ctypes.data))
@@ -874,7 +878,7 @@ class Pages:
 
     def own(self, page: int) -> int:
         """The page to write in place of ``page``: itself, or a new one to copy it to."""
-        if page not in _INT32:
+        if not _fits(page):
             raise ValueError(f"page must be one of the {self.pages}, not {page}")
         out = C.c_int32()
         _check(_lib.uw_pages_own(self._h, page, C.byref(out)))

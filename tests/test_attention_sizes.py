@@ -69,3 +69,19 @@ def test_pages_are_not_cut():
     assert p.left == 4
     with pytest.raises(ValueError):
         uw.Pages((1 << 64) + 4)
+
+
+@pytest.mark.timeout(20)
+@pytest.mark.parametrize("kind", [np.int32, np.int64, np.uint8])
+def test_numbers_as_arrays_hold_them(kind):
+    """Page numbers and sizes that come out of arrays."""
+    p = uw.Pages(kind(6))
+    pages = p.take(kind(4))
+    assert p.holders(kind(3)) == 1 and p.own(kind(3)) == 3
+    assert p.own(pages[2]) == 2 and p.holders(pages[2]) == 1
+    sizes = [kind(v) for v in (6, 2, 8, 2, 64, 3, 100)]
+    for f in (uw.attention_workspace_bytes, uw.attend_workspace_bytes):
+        assert f(*sizes) == f(*[int(v) for v in sizes])
+    for f in (p.own, p.holders, p.take):
+        with pytest.raises(TypeError):
+            f(1.0)
